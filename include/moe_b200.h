@@ -425,6 +425,128 @@ MOE_API int moe_expert_ffn_slots(const moe_dims* dims, const moe_bf16* x_perm, c
                                  const int32_t* expert_slot, int n_slots, const moe_bf16* W13c, const moe_bf16* W2c,
                                  moe_bf16* h, float* y_perm, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- training
+ * The gradients of the layer's steps, and the norm in front of it ([P2]
+ * sections 1 and 2 give the forward formulas these differentiate; the pages
+ * have no counterpart of the norm).  One training step of a sublayer
+ * out = x + moe(layernorm(x)) calls, in this order:
+ *   moe_layernorm, moe_route, moe_permute, moe_ffn_train, moe_combine;
+ *   moe_combine_backward, moe_ffn_backward, moe_route_backward (with the
+ *   dispatch's gradient in it; moe_permute_backward alone when the router is
+ *   frozen), moe_layernorm_backward (with the residual's gradient added).
+ * Only forward buffers named below have to be kept in between.
+ *
+ * Rows of grouped buffers behind the last kept row are never written.  A
+ * gradient is written, not accumulated.  Matrix operands are bf16, sums
+ * fp32; an output is rounded once, to nearest even.  Results do not depend
+ * on timing: no atomics, every sum has a fixed order.
+ *
+ * `ws` of these calls starts with a status word that
+ * moe_reset_device_status and moe_get_device_status act on; clear it once
+ * after allocating.  Two calls in flight need a workspace each. */
+#define MOE_STATUS_BYTES 256
+
+/* Layer norm over the last axis: y = (x - mean) * rstd * gamma + beta with
+ * rstd = 1 / sqrt(var + eps), var the mean squared deviation.
+ *   x, y         [T, d_model]: bf16 with x_is_bf16 != 0, else fp32
+ *   gamma, beta  [d_model]: bf16 with w_is_bf16 != 0, else fp32; either may
+ *                be NULL (1 and 0)
+ *   mean, rstd   [T] fp32 out or NULL: what the backward pass needs
+ * y may be x.  eps >= 0.  d_model: a multiple of 16 up to 16384, larger ones
+ * return MOE_EUNSUPPORTED. */
+MOE_API int moe_layernorm(int64_t T, int d_model, const void* x, int x_is_bf16, const void* gamma, const void* beta,
+                          int w_is_bf16, float eps, void* y, float* mean, float* rstd, void* stream);
+
+/* Its backward pass.
+ *   dy, x, dx    [T, d_model] (type as above); x is the forward's input
+ *   dx_add       [T, d_model] same type or NULL: added to dx before the one
+ *                rounding (the gradient that reaches x past the norm)
+ *   dgamma, dbeta [d_model] out, the type of gamma (w_is_bf16), summed in
+ *                fp32 over the tokens in a fixed order
+ * Any of dx, dgamma, dbeta may be NULL, not all three.  dx may be dy or
+ * dx_add.  ws (moe_layernorm_workspace_size bytes) may be NULL without dgamma
+ * and dbeta; its status word is left alone (nothing here waits). */
+MOE_API int moe_layernorm_workspace_size(int64_t T, int d_model, size_t* bytes);
+MOE_API int moe_layernorm_backward(int64_t T, int d_model, const void* dy, const void* x, int x_is_bf16, const void* gamma,
+                                   int w_is_bf16, const float* mean, const float* rstd, const void* dx_add, void* dx,
+                                   void* dgamma, void* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/* The experts' gated feed-forward block, from weights in their own layout
+ * (an optimizer rewrites them every step: nothing is packed), keeping what
+ * the backward pass needs.  G = X W1, U = X W3, H = silu(G) * U in one
+ * kernel, then Y = H W2, for the rows of each expert.
+ *   x_perm   [T*K, d_model] bf16, offsets [E+1] int32 (device), as moe_permute
+ *            writes them.  E = 1 with offsets {0, T*K} is a dense block.
+ *   W1, W3   [E, d_model, d_ff] bf16;  W2 [E, d_ff, d_model] bf16
+ *   gu       [T*K, 2*d_ff] bf16 out: G in columns 0.., U in columns d_ff..
+ *   h        [T*K, d_ff] bf16 out: H from the unrounded G and U
+ *   y_perm   [T*K, d_model] fp32 out: H W2 of the rounded H
+ * ws: MOE_STATUS_BYTES bytes. */
+MOE_API int moe_ffn_train(const moe_dims* dims, const moe_bf16* x_perm, const int32_t* offsets, const moe_bf16* W1,
+                          const moe_bf16* W3, const moe_bf16* W2, moe_bf16* gu, moe_bf16* h, float* y_perm, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* Its backward pass.  With dH = dY W2^T and s = sigmoid(G):
+ *   dG = dH * U * s * (1 + G * (1 - s)),  dU = dH * G * s
+ *   dX = dG W1^T + dU W3^T,  dW1 = X^T dG,  dW3 = X^T dU,  dW2 = H^T dY
+ *   dy_perm  [T*K, d_model] bf16 (moe_combine_backward)
+ *   x_perm, offsets, W1, W3, W2, gu, h   as in moe_ffn_train
+ *   dgu      [T*K, 2*d_ff] bf16 out: dG and dU, rounded once; the products
+ *            above use the rounded values
+ *   dx_perm  [T*K, d_model] bf16 out, or NULL
+ *   dW1, dW3, dW2  out, bf16 with dw_is_bf16 != 0, else fp32; zero for an
+ *            expert without rows.  dW1 and dW3 both or neither; NULL: frozen
+ * An input that no wanted output needs may be NULL (x_perm, W1, W3, h).
+ * ws: MOE_STATUS_BYTES bytes. */
+MOE_API int moe_ffn_backward(const moe_dims* dims, const moe_bf16* dy_perm, const moe_bf16* x_perm, const int32_t* offsets,
+                             const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2, const moe_bf16* gu, const moe_bf16* h,
+                             moe_bf16* dgu, moe_bf16* dx_perm, void* dW1, void* dW3, void* dW2, int dw_is_bf16, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* Gradient of moe_combine: for each kept slot with r = inv[t,k]
+ *   dy_perm[r] = topk_w[t,k] * dy[t],  dtopk_w[t,k] = <dy[t], y_perm[r]>.
+ *   dy        [T, d_model]: bf16 with dy_is_bf16 != 0, else fp32
+ *   dy_perm   [T*K, d_model] bf16 out (the experts' backward operand)
+ *   dtopk_w   [T, K] fp32 out or NULL; 0 for a dropped slot.  y_perm
+ *             [T*K, d_model] fp32 is read only for it
+ * An inv outside [0, T*K) counts as dropped. */
+MOE_API int moe_combine_backward(const moe_dims* dims, const void* dy, int dy_is_bf16, const float* y_perm,
+                                 const int32_t* inv, const float* topk_w, moe_bf16* dy_perm, float* dtopk_w, void* stream);
+
+/* Gradient of moe_permute's row gather: dx[t] = sum over the kept slots of
+ * dx_perm[inv[t,k]], in slot order in fp32; dx [T, d_model] fp32, or bf16
+ * with dx_is_bf16 != 0. */
+MOE_API int moe_permute_backward(const moe_dims* dims, const moe_bf16* dx_perm, const int32_t* inv, void* dx,
+                                 int dx_is_bf16, void* stream);
+
+/* Gradient of moe_route.  With p the softmax of the unbiased logits, lse
+ * their log-sum-exp and f_e = counts_e / (T K) (constant, as in the balance
+ * loss), the logits' gradient is
+ *   dl[t,e] = sum_{k: idx[t,k] = e} w[t,k] (dw[t,k] - sum_j w[t,j] dw[t,j])
+ *           + aux_coef * E / T * p[t,e] * (f_e - sum_i f_i p[t,i])
+ *           + z_coef * 2 / T * lse[t] * p[t,e]
+ * (the top-K softmax; aux and z_loss of moe_layer_outputs, weighted by
+ * aux_coef and z_coef in the training loss), and
+ *   dx[t] = sum of dx_perm[inv[t,k]] over the kept slots + dl[t] Wr^T
+ *   dWr   = x^T dl.
+ *   x, Wr, topk_idx, topk_w   as in moe_route (topk_w: its output)
+ *   logits    [T, E] fp32, needed with a non-zero coefficient
+ *   counts    [E] int32, needed with aux_coef != 0
+ *   dtopk_w   [T, K] fp32 or NULL (zero)
+ *   dx_perm, inv   both or neither (no rows are added)
+ *   dx        [T, d_model] out: bf16 with dx_is_bf16 != 0, else fp32; or NULL
+ *   dWr       [d_model, E] out: bf16 with dw_is_bf16 != 0, else fp32; or NULL
+ *   dlogits   [T, E] fp32 out, or NULL
+ * The two products multiply dl rounded to bf16; the bias of moe_route has no
+ * gradient (moe_bias_update moves it).  ws:
+ * moe_route_backward_workspace_size bytes. */
+MOE_API int moe_route_backward_workspace_size(const moe_dims* dims, size_t* bytes);
+MOE_API int moe_route_backward(const moe_dims* dims, const moe_bf16* x, const moe_bf16* Wr, const float* logits,
+                               const int32_t* topk_idx, const float* topk_w, const float* dtopk_w, const int32_t* counts,
+                               float aux_coef, float z_coef, const moe_bf16* dx_perm, const int32_t* inv, void* dx,
+                               int dx_is_bf16, void* dWr, int dw_is_bf16, float* dlogits, void* ws, size_t ws_bytes,
+                               void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -36,8 +36,12 @@ EXPORTED = [
     "moe_layer_launch_count", "moe_packed_weight_bytes", "moe_permute_noalloc", "moe_ffn_kernel",
     "moe_chunked_workspace_size", "moe_layer_forward_chunked", "moe_layer_chunked_launch_count",
     "moe_test_set_wait_limits", "moe_ep_regroup", "moe_int4_bytes", "moe_int4_pack", "moe_int4_unpack",
-    "moe_expert_ffn_slots",
+    "moe_expert_ffn_slots", "moe_layernorm", "moe_layernorm_workspace_size", "moe_layernorm_backward",
+    "moe_ffn_train", "moe_ffn_backward", "moe_combine_backward", "moe_permute_backward",
+    "moe_route_backward_workspace_size", "moe_route_backward",
 ]
+LAYERNORM_MAX_WIDTH = 16384
+STATUS_BYTES = 256  # workspace of moe_ffn_train and moe_ffn_backward
 NUM_STAGE_EVENTS = 6
 
 
@@ -103,6 +107,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_int4_unpack": (I, [dims_p, I, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32),
                                 P, P, P, P, I, P, P, P]),
         "moe_expert_ffn_slots": (I, [dims_p, P, P, P, I, P, P, P, P, P, SZ, P]),
+        "moe_layernorm": (I, [I64, I, P, I, P, P, I, F, P, P, P, P]),
+        "moe_layernorm_workspace_size": (I, [I64, I, ctypes.POINTER(SZ)]),
+        "moe_layernorm_backward": (I, [I64, I, P, P, I, P, I, P, P, P, P, P, P, P, SZ, P]),
+        "moe_ffn_train": (I, [dims_p, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_ffn_backward": (I, [dims_p, P, P, P, P, P, P, P, P, P, P, P, P, P, I, P, SZ, P]),
+        "moe_combine_backward": (I, [dims_p, P, I, P, P, P, P, P, P]),
+        "moe_permute_backward": (I, [dims_p, P, P, P, I, P]),
+        "moe_route_backward_workspace_size": (I, [dims_p, ctypes.POINTER(SZ)]),
+        "moe_route_backward": (I, [dims_p, P, P, P, P, P, P, P, F, F, P, P, P, I, P, I, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -408,6 +421,163 @@ def moe_expert_ffn_slots(dims, x_perm, offsets, expert_slot, n_slots: int, W13c,
         ctypes.byref(_dims(dims)), _ptr(x_perm, BF16, "x_perm"), _ptr(offsets, I32, "offsets"),
         _ptr(expert_slot, I32, "expert_slot"), int(n_slots), _ptr(W13c, BF16, "W13c"), _ptr(W2c, BF16, "W2c"),
         _ptr(h, BF16, "h"), _ptr(y_perm, F32, "y_perm"), _ptr(ws, None, "ws"), ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- training
+
+class _On:
+    """Checks one call's tensors and launches it on their device and stream."""
+
+    def __init__(self, anchor, stream):
+        if not isinstance(anchor, torch.Tensor) or anchor.device.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        self.device, self.stream = anchor.device, stream
+
+    def ptr(self, t, numel: int, name: str, dtype=None, optional: bool = False):
+        """Address of a contiguous tensor of at least `numel` values on the call's device."""
+        if t is None:
+            if optional:
+                return None
+            raise ValueError(f"{name}: required")
+        p = _ptr(t, dtype, name)
+        if t.device != self.device:
+            raise ValueError(f"{name}: on {t.device}, the call's other tensors are on {self.device}")
+        if t.numel() < numel:
+            raise ValueError(f"{name}: {t.numel()} values, {numel} needed")
+        return p
+
+    def either(self, t, numel: int, name: str, like=None, optional: bool = False):
+        """Address and is_bf16 flag of a bf16 or fp32 tensor (of `like`'s type, where given)."""
+        if t is None and optional:
+            return None, 0
+        if isinstance(t, torch.Tensor) and t.dtype not in (BF16, F32):
+            raise TypeError(f"{name}: expected {BF16} or {F32}, got {t.dtype}")
+        return self.ptr(t, numel, name, None if like is None else like.dtype, optional), int(t is not None and t.dtype == BF16)
+
+    def call(self, name: str, *args):
+        fn = getattr(load(), name)
+        if torch.cuda.current_device() == self.device.index:
+            _check(name, fn(*args, self._stream()))
+        else:
+            with torch.cuda.device(self.device):
+                _check(name, fn(*args, self._stream()))
+
+    def _stream(self):
+        return torch.cuda.current_stream(self.device).cuda_stream if self.stream is None else _stream(self.stream)
+
+
+def _rows_of(x, name):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError(f"{name}: expected a tensor [..., d_model]")
+    return x.numel() // x.shape[-1], int(x.shape[-1])
+
+
+def moe_layernorm(x, gamma, beta, eps: float, y, mean=None, rstd=None, stream=None):
+    """Layer norm over x's last axis (x, y bf16 or fp32; gamma, beta both bf16 or both fp32, or None)."""
+    on = _On(x, stream)
+    T, d = _rows_of(x, "x")
+    xp, xb = on.either(x, T * d, "x")
+    w = gamma if gamma is not None else beta
+    gp, gb = on.either(gamma, d, "gamma", w, True)
+    bp, bb = on.either(beta, d, "beta", w, True)
+    on.call("moe_layernorm", T, d, xp, xb, gp, bp, gb | bb, eps, on.ptr(y, T * d, "y", x.dtype),
+            on.ptr(mean, T, "mean", F32, True), on.ptr(rstd, T, "rstd", F32, True))
+
+
+def moe_layernorm_workspace_size(T: int, d_model: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_layernorm_workspace_size", load().moe_layernorm_workspace_size(T, d_model, ctypes.byref(n)))
+    return int(n.value)
+
+
+def moe_layernorm_backward(dy, x, gamma, mean, rstd, dx_add, dx, dgamma, dbeta, ws, stream=None):
+    """Gradients of moe_layernorm; dx_add is added to dx (see the header)."""
+    on = _On(x, stream)
+    T, d = _rows_of(x, "x")
+    xp, xb = on.either(x, T * d, "x")
+    w = next((t for t in (gamma, dgamma, dbeta) if t is not None), None)
+    gp, gb = on.either(gamma, d, "gamma", w, True)
+    dgp, dgb = on.either(dgamma, d, "dgamma", w, True)
+    dbp, dbb = on.either(dbeta, d, "dbeta", w, True)
+    on.call("moe_layernorm_backward", T, d, on.ptr(dy, T * d, "dy", x.dtype), xp, xb, gp, gb | dgb | dbb,
+            on.ptr(mean, T, "mean", F32), on.ptr(rstd, T, "rstd", F32), on.ptr(dx_add, T * d, "dx_add", x.dtype, True),
+            on.ptr(dx, T * d, "dx", x.dtype, True), dgp, dbp, on.ptr(ws, 0, "ws", torch.uint8, True),
+            0 if ws is None else ws.numel())
+
+
+def moe_ffn_train(dims, x_perm, offsets, W1, W3, W2, gu, h, y_perm, ws, stream=None):
+    """The experts' gated FFN from unpacked weights, keeping gu and h for moe_ffn_backward."""
+    on, c = _On(x_perm, stream), _dims(dims)
+    A, d, f, E = c.T * c.K, c.d_model, c.d_ff, c.E
+    on.call("moe_ffn_train", ctypes.byref(c), on.ptr(x_perm, A * d, "x_perm", BF16), on.ptr(offsets, E + 1, "offsets", I32),
+            on.ptr(W1, E * d * f, "W1", BF16), on.ptr(W3, E * d * f, "W3", BF16), on.ptr(W2, E * f * d, "W2", BF16),
+            on.ptr(gu, A * 2 * f, "gu", BF16), on.ptr(h, A * f, "h", BF16), on.ptr(y_perm, A * d, "y_perm", F32),
+            on.ptr(ws, 0, "ws", torch.uint8), ws.numel())
+
+
+def moe_ffn_backward(dims, dy_perm, x_perm, offsets, W1, W3, W2, gu, h, dgu, dx_perm, dW1, dW3, dW2, ws, stream=None):
+    """Gradients of moe_ffn_train (dW1, dW3, dW2 all bf16 or all fp32; None: not wanted)."""
+    on, c = _On(dy_perm, stream), _dims(dims)
+    A, d, f, E = c.T * c.K, c.d_model, c.d_ff, c.E
+    like = dW1 if dW1 is not None else dW2
+    p1, b1 = on.either(dW1, E * d * f, "dW1", like, True)
+    p3, b3 = on.either(dW3, E * d * f, "dW3", like, True)
+    p2, b2 = on.either(dW2, E * f * d, "dW2", like, True)
+    on.call("moe_ffn_backward", ctypes.byref(c), on.ptr(dy_perm, A * d, "dy_perm", BF16),
+            on.ptr(x_perm, A * d, "x_perm", BF16, True), on.ptr(offsets, E + 1, "offsets", I32),
+            on.ptr(W1, E * d * f, "W1", BF16, True), on.ptr(W3, E * d * f, "W3", BF16, True), on.ptr(W2, E * f * d, "W2", BF16),
+            on.ptr(gu, A * 2 * f, "gu", BF16), on.ptr(h, A * f, "h", BF16, True), on.ptr(dgu, A * 2 * f, "dgu", BF16),
+            on.ptr(dx_perm, A * d, "dx_perm", BF16, True), p1, p3, p2, b1 | b3 | b2, on.ptr(ws, 0, "ws", torch.uint8), ws.numel())
+
+
+def moe_combine_backward(dims, dy, y_perm, inv, topk_w, dy_perm, dtopk_w=None, stream=None):
+    """Gradients of moe_combine (dy bf16 or fp32; y_perm is read only for dtopk_w)."""
+    on, c = _On(dy, stream), _dims(dims)
+    T, A, d = c.T, c.T * c.K, c.d_model
+    dyp, db = on.either(dy, T * d, "dy")
+    on.call("moe_combine_backward", ctypes.byref(c), dyp, db, on.ptr(y_perm, A * d, "y_perm", F32, dtopk_w is None),
+            on.ptr(inv, A, "inv", I32), on.ptr(topk_w, A, "topk_w", F32), on.ptr(dy_perm, A * d, "dy_perm", BF16),
+            on.ptr(dtopk_w, A, "dtopk_w", F32, True))
+
+
+def moe_permute_backward(dims, dx_perm, inv, dx, stream=None):
+    """Rows' gradients summed back to their tokens (dx bf16 or fp32)."""
+    on, c = _On(dx_perm, stream), _dims(dims)
+    A, d = c.T * c.K, c.d_model
+    dxp, db = on.either(dx, c.T * d, "dx")
+    on.call("moe_permute_backward", ctypes.byref(c), on.ptr(dx_perm, A * d, "dx_perm", BF16), on.ptr(inv, A, "inv", I32), dxp, db)
+
+
+def moe_route_backward_workspace_size(dims) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_route_backward_workspace_size",
+           load().moe_route_backward_workspace_size(ctypes.byref(_dims(dims)), ctypes.byref(n)))
+    return int(n.value)
+
+
+def moe_route_backward(dims, x, Wr, logits, topk_idx, topk_w, dtopk_w, counts, aux_coef: float, z_coef: float, dx_perm, inv,
+                       dx, dWr, dlogits, ws, stream=None):
+    """Gradients of moe_route, with the dispatch's gradient added into dx where dx_perm and inv are given."""
+    on, c = _On(ws, stream), _dims(dims)
+    T, A, d, E = c.T, c.T * c.K, c.d_model, c.E
+    dxp, xb = on.either(dx, T * d, "dx", None, True)
+    dwp, wb = on.either(dWr, d * E, "dWr", None, True)
+    on.call("moe_route_backward", ctypes.byref(c), on.ptr(x, T * d, "x", BF16, True), on.ptr(Wr, d * E, "Wr", BF16, True),
+            on.ptr(logits, T * E, "logits", F32, True), on.ptr(topk_idx, A, "topk_idx", I32, True),
+            on.ptr(topk_w, A, "topk_w", F32, True), on.ptr(dtopk_w, A, "dtopk_w", F32, True),
+            on.ptr(counts, E, "counts", I32, True), aux_coef, z_coef, on.ptr(dx_perm, A * d, "dx_perm", BF16, True),
+            on.ptr(inv, A, "inv", I32, True), dxp, xb, dwp, wb, on.ptr(dlogits, T * E, "dlogits", F32, True),
+            on.ptr(ws, 0, "ws", torch.uint8), ws.numel())
+
+
+def alloc_train_workspace(dims, device="cuda") -> torch.Tensor:
+    """One workspace (uint8, status word clear) for every training call at these dims; calls on one stream may
+    share it."""
+    c = _dims(dims)
+    n = moe_route_backward_workspace_size(c)
+    if c.d_model <= LAYERNORM_MAX_WIDTH:
+        n = max(n, moe_layernorm_workspace_size(c.T, c.d_model))
+    return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 # ---------------------------------------------------------------- helpers

@@ -7,7 +7,7 @@
 
 #include <atomic>
 
-#include "../../include/moe_b200.h"
+#include "abi_checks.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -30,26 +30,8 @@ WaitSettings wait_settings() {
 
 namespace {
 
-constexpr int kVersion = 200;  // 2.00: y_is_bf16 in moe_combine and both layer calls; MOE_EINDEX;
+constexpr int kVersion = 210;  // 2.10: the training entry points.  2.00: y_is_bf16 in moe_combine and both layer calls; MOE_EINDEX;
                                 // moe_test_set_wait_limits.  1.01: P_topk, aux_topk, z_loss; chunked layer
-constexpr int64_t kMaxT = int64_t(1) << 24;
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int check_dims(const moe_dims* d) {
-    if (!d) return MOE_EINVAL;
-    if (d->T < 1 || d->T > kMaxT) return MOE_EINVAL;
-    if (d->E < 1 || d->E > 256) return MOE_EINVAL;
-    if (d->K < 1 || d->K > d->E || d->K > 16) return MOE_EINVAL;
-    if (d->d_model < 16 || d->d_ff < 16) return MOE_EINVAL;
-    if (d->d_model > (1 << 16) || d->d_ff > (1 << 17)) return MOE_EINVAL;
-    if (d->d_model % 16 != 0 || d->d_ff % 16 != 0) return MOE_EUNSUPPORTED;
-    if (std::isnan(d->capacity_factor)) return MOE_EINVAL;
-    return MOE_OK;
-}
-
 // C = ceil(cf * T * K / E) on the exact binary value of cf; -1 = no limit.
 int64_t capacity_of(const moe_dims* d) {
     const double cf = d->capacity_factor;
@@ -185,12 +167,6 @@ T* at(void* ws, size_t off) {
     return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
 }
 
-int map_launch(int r) {
-    if (r == 0) return MOE_OK;
-    if (r == -2) return MOE_EUNSUPPORTED;
-    return MOE_ECUDA;
-}
-
 // Workspace of the chunked layer: one chunk's layer workspace at offset 0
 // (large enough for a full chunk and for the last, shorter one; its status
 // word is the workspace's), then the whole batch's routing state.
@@ -238,12 +214,6 @@ int check_ws(const moe_dims* d, void* ws, size_t ws_bytes) {
     if (ws_bytes < layout_of(d).total) return MOE_EWORKSPACE;
     return MOE_OK;
 }
-
-#define MOE_TRY(expr)               \
-    do {                            \
-        int _s = (expr);            \
-        if (_s != MOE_OK) return _s; \
-    } while (0)
 
 int do_route(const moe_dims* d, const Layout& L, const bf16* x, const bf16* Wr, const float* bias, float* logits,
              int32_t* idx, float* w, float* prob_mean, void* ws, cudaStream_t st, bool finalize = true) {

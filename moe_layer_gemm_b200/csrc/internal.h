@@ -213,4 +213,41 @@ int launch_pack(const bf16* W1, const bf16* W3, const bf16* W2, int E, int d, in
 size_t packed_w13_bytes(int E, int d, int f);
 size_t packed_w2_bytes(int E, int d, int f);
 
+// ------------------------------------------------------------ training: norm (norm.cu)
+bool layernorm_supported(int d);
+int layernorm_blocks(int64_t T, int d);  // partial rows [2 d] fp32 of the weight's gradients
+int launch_layernorm(const void* x, bool x_bf16, const void* gamma, const void* beta, bool w_bf16, float eps, int64_t T,
+                     int d, void* y, float* mean, float* rstd, cudaStream_t st);
+int launch_layernorm_backward(const void* dy, const void* x, bool x_bf16, const void* gamma, bool w_bf16, const float* mean,
+                              const float* rstd, const void* dx_add, int64_t T, int d, void* dx, void* dgamma, void* dbeta,
+                              float* part, cudaStream_t st);
+
+// ------------------------------------------------------------ training: experts (train_gemm.cu)
+// Rows grouped by expert (device offsets), weights as [E, rows, cols].
+int launch_train_gate(const bf16* x, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W1,
+                      const bf16* W3, bf16* gu, bf16* h, int* status, cudaStream_t st);
+int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2, float* y,
+                      int* status, cudaStream_t st);
+int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2,
+                       const bf16* gu, bf16* dgu, int* status, cudaStream_t st);
+int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W1,
+                    const bf16* W3, bf16* dx, int* status, cudaStream_t st);
+// out_j[g] = left[rows of g]^T right_j[rows of g]; groups by offsets, or of `chunk` rows when off is nullptr.
+int launch_train_dw(const bf16* left, int m_cols, const bf16* right0, const bf16* right1, int64_t right_ld, int n_cols,
+                    const int32_t* off, int64_t chunk, int64_t rows, int G, void* out0, void* out1, int64_t out_ld,
+                    bool out_bf16, int* status, cudaStream_t st);
+// dx[t] = dl[t] Wr^T + the sum of token t's rows (rows may be nullptr).
+int launch_train_router_dx(const bf16* dl, int64_t T, int dl_ld, const bf16* Wr, int wr_ld, int E, int d, const bf16* rows,
+                           const int32_t* inv, int K, void* dx, bool dx_bf16, int* status, cudaStream_t st);
+
+// ------------------------------------------------------------ training: around the experts (train.cu)
+int launch_combine_backward(const void* dy, bool dy_bf16, const float* y_perm, const int32_t* inv, const float* w, int64_t T,
+                            int d, int K, bf16* dy_perm, float* dw, cudaStream_t st);
+int launch_permute_backward(const bf16* dx_perm, const int32_t* inv, int64_t T, int d, int K, void* dx, bool dx_bf16,
+                            cudaStream_t st);
+int launch_route_backward(const float* logits, const int32_t* idx, const float* w, const float* dw, const int32_t* counts,
+                          float aux, float zc, int64_t T, int E, int K, int ld, float* dlogits, bf16* dl16, cudaStream_t st);
+int launch_pad_router(const bf16* Wr, int d, int E, int ld, bf16* out, cudaStream_t st);
+int launch_router_weight(const float* part, int S, int d, int E, int ld, void* out, bool out_bf16, cudaStream_t st);
+
 }  // namespace moe

@@ -1,0 +1,222 @@
+// Gradients of the steps around the experts: combine, dispatch and router.
+//
+//   combine   dy_perm[r] = w[t,k] * dy[t],  dw[t,k] = <dy[t], y_perm[r]>,  r = inv[t,k]
+//   dispatch  dx[t] = sum over the kept slots k of dx_perm[inv[t,k]]
+//   router    dl[t,e] = sum over the slots k that chose e of w[t,k] (dw[t,k] - sum_j w[t,j] dw[t,j])
+//                     + aux * E / T * p[t,e] * (f_e - sum_i f_i p[t,i])
+//                     + zc * 2 / T * lse[t] * p[t,e]
+// with p and lse the softmax and log-sum-exp of the unbiased logits and
+// f_e = counts_e / (T K), a constant as in the balance loss itself.  All of
+// them are bound by memory: a token's row is read once, all its slots' rows
+// are in flight together, and every sum is fp32 in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "vec.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxK = 16;
+
+// A block per token.  Slot k's dot product is summed per thread over its
+// columns, then over the warps in order.
+template <typename Y>
+__global__ void __launch_bounds__(256)
+combine_backward_kernel(const Y* __restrict__ dy, const float* __restrict__ y_perm, const int32_t* __restrict__ inv,
+                        const float* __restrict__ w, int64_t rows, int d, int K, bf16* __restrict__ dy_perm,
+                        float* __restrict__ dw) {
+    __shared__ float red[kMaxK][8];
+    const int64_t t = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int k = 0; k < K; ++k) {
+        const int64_t r = inv[t * K + k];
+        float dot = 0.f;
+        if (r >= 0 && r < rows) {
+            const float wk = w[t * K + k];
+            for (int c = threadIdx.x * 8; c < d; c += blockDim.x * 8) {
+                float g[8], o[8], y[8];
+                load8(dy + t * d + c, g);
+                if (dw) load8(y_perm + r * d + c, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    o[i] = wk * g[i];
+                    if (dw) dot += g[i] * y[i];
+                }
+                put8(dy_perm + r * d + c, o);
+            }
+        }
+        if (dw) {
+            dot = warp_sum(dot);
+            if (lane == 0) red[k][warp] = dot;
+        }
+    }
+    if (!dw) return;
+    __syncthreads();
+    if (threadIdx.x < K) {
+        float s = 0.f;
+        for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += red[threadIdx.x][i];
+        dw[t * K + threadIdx.x] = s;
+    }
+}
+
+template <typename X>
+__global__ void __launch_bounds__(256)
+permute_backward_kernel(const bf16* __restrict__ dx_perm, const int32_t* __restrict__ inv, int64_t rows, int d, int K,
+                        X* __restrict__ dx) {
+    const int64_t t = blockIdx.x;
+    for (int c = threadIdx.x * 8; c < d; c += blockDim.x * 8) {
+        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < K; ++k) {
+            const int64_t r = inv[t * K + k];
+            if (r < 0 || r >= rows) continue;
+            float v[8];
+            load8(dx_perm + r * d + c, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] += v[i];
+        }
+        put8(dx + t * d + c, s);
+    }
+}
+
+// A warp per token; lane l owns experts l, l + 32, ...  The bf16 copy [T, ld]
+// (columns E.. zero) is what the two router products multiply: a rounding of
+// 2^-9 of each value, as for every other operand of the tensor cores.
+__global__ void __launch_bounds__(256)
+route_backward_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx, const float* __restrict__ w,
+                      const float* __restrict__ dw, const int32_t* __restrict__ counts, float aux, float zc, int64_t T, int E,
+                      int K, int ld, float* __restrict__ dlogits, bf16* __restrict__ dl16) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (t >= T) return;
+    float dl[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dl[j] = 0.f;
+    if (logits) {
+        float l[8], p[8];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = lane + 32 * j;
+            l[j] = e < E ? logits[t * E + e] : -INFINITY;
+            mx = fmaxf(mx, l[j]);
+        }
+        mx = warp_max(mx);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            p[j] = lane + 32 * j < E ? expf(l[j] - mx) : 0.f;
+            sum += p[j];
+        }
+        sum = warp_sum(sum);
+        const float inv_sum = 1.0f / sum, lse = mx + logf(sum);
+        const float invA = 1.0f / (static_cast<float>(T) * static_cast<float>(K));
+        float f[8];
+        float fp = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = lane + 32 * j;
+            p[j] *= inv_sum;
+            f[j] = counts && e < E ? static_cast<float>(counts[e]) * invA : 0.f;
+            fp += f[j] * p[j];
+        }
+        fp = warp_sum(fp);
+        const float ca = aux * static_cast<float>(E) / static_cast<float>(T), cz = 2.0f * zc / static_cast<float>(T) * lse;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dl[j] = p[j] * (ca * (f[j] - fp) + cz);
+    }
+    if (dw) {
+        const float wk = lane < K ? w[t * K + lane] : 0.f, dk = lane < K ? dw[t * K + lane] : 0.f;
+        const int ek = lane < K ? idx[t * K + lane] : -1;
+        const float g = wk * (dk - warp_sum(wk * dk));
+        for (int k = 0; k < K; ++k) {
+            const int e = __shfl_sync(0xffffffffu, ek, k);
+            const float gk = __shfl_sync(0xffffffffu, g, k);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e == lane + 32 * j) dl[j] += gk;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int e = lane + 32 * j;
+        if (dlogits && e < E) dlogits[t * E + e] = dl[j];
+        if (dl16 && e < ld) dl16[t * ld + e] = __float2bfloat16_rn(e < E ? dl[j] : 0.f);
+    }
+}
+
+// Router weight [d, E] with rows of ld elements (TMA reads rows of a multiple
+// of 16 bytes); columns E.. are zero.
+__global__ void __launch_bounds__(256)
+pad_router_kernel(const bf16* __restrict__ Wr, int64_t n, int E, int ld, bf16* __restrict__ out) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t r = i / ld;
+    const int c = static_cast<int>(i - r * ld);
+    out[i] = c < E ? Wr[r * E + c] : __float2bfloat16_rn(0.f);
+}
+
+// dWr [d, E] = the token chunks' partial products [S, d, ld], summed in chunk order.
+template <typename W>
+__global__ void __launch_bounds__(256)
+router_weight_kernel(const float* __restrict__ part, int S, int64_t stride, int64_t n, int E, int ld, W* __restrict__ out) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t r = i / E;
+    const int64_t at = r * ld + (i - r * E);
+    float s = 0.f;
+    for (int j = 0; j < S; ++j) s += part[j * stride + at];
+    out[i] = static_cast<W>(s);
+}
+
+int row_threads(int d) {
+    const int t = (d / 8 + 31) / 32 * 32;
+    return t < 32 ? 32 : (t > 256 ? 256 : t);
+}
+int done() { return cudaGetLastError() == cudaSuccess ? 0 : -3; }
+
+}  // namespace
+
+int launch_combine_backward(const void* dy, bool dy_bf16, const float* y_perm, const int32_t* inv, const float* w, int64_t T,
+                            int d, int K, bf16* dy_perm, float* dw, cudaStream_t st) {
+    const unsigned grid = static_cast<unsigned>(T);
+    if (dy_bf16)
+        combine_backward_kernel<<<grid, row_threads(d), 0, st>>>(static_cast<const bf16*>(dy), y_perm, inv, w, T * K, d, K, dy_perm, dw);
+    else
+        combine_backward_kernel<<<grid, row_threads(d), 0, st>>>(static_cast<const float*>(dy), y_perm, inv, w, T * K, d, K, dy_perm, dw);
+    return done();
+}
+
+int launch_permute_backward(const bf16* dx_perm, const int32_t* inv, int64_t T, int d, int K, void* dx, bool dx_bf16,
+                            cudaStream_t st) {
+    const unsigned grid = static_cast<unsigned>(T);
+    if (dx_bf16)
+        permute_backward_kernel<<<grid, row_threads(d), 0, st>>>(dx_perm, inv, T * K, d, K, static_cast<bf16*>(dx));
+    else
+        permute_backward_kernel<<<grid, row_threads(d), 0, st>>>(dx_perm, inv, T * K, d, K, static_cast<float*>(dx));
+    return done();
+}
+
+int launch_route_backward(const float* logits, const int32_t* idx, const float* w, const float* dw, const int32_t* counts,
+                          float aux, float zc, int64_t T, int E, int K, int ld, float* dlogits, bf16* dl16, cudaStream_t st) {
+    route_backward_kernel<<<static_cast<unsigned>((T + 7) / 8), 256, 0, st>>>(logits, idx, w, dw, counts, aux, zc, T, E, K, ld, dlogits, dl16);
+    return done();
+}
+
+int launch_pad_router(const bf16* Wr, int d, int E, int ld, bf16* out, cudaStream_t st) {
+    const int64_t n = static_cast<int64_t>(d) * ld;
+    pad_router_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, st>>>(Wr, n, E, ld, out);
+    return done();
+}
+
+int launch_router_weight(const float* part, int S, int d, int E, int ld, void* out, bool out_bf16, cudaStream_t st) {
+    const int64_t n = static_cast<int64_t>(d) * E, stride = static_cast<int64_t>(d) * ld;
+    const unsigned grid = static_cast<unsigned>((n + 255) / 256);
+    if (out_bf16) router_weight_kernel<<<grid, 256, 0, st>>>(part, S, stride, n, E, ld, static_cast<bf16*>(out));
+    else router_weight_kernel<<<grid, 256, 0, st>>>(part, S, stride, n, E, ld, static_cast<float*>(out));
+    return done();
+}
+
+}  // namespace moe

@@ -1,0 +1,772 @@
+// Grouped matrix products of a training step on CTA pairs (tcgen05
+// cta_group::2), reading the weights in their own [E, rows, cols] layout:
+// an optimizer rewrites them every step, so nothing is packed beforehand.
+//
+// With g the experts, X_g the rows of expert g and the weights
+// W1, W3 [d, f], W2 [f, d]:
+//   gate    G = X W1, U = X W3, H = silu(G) * U        (one launch)
+//   down    Y = H W2
+//   dgate   dH = dY W2^T, then dG, dU from dH, G, U    (one launch)
+//   dx      dX = dG W1^T + dU W3^T                     (one accumulation)
+//   dw13    dW1 = X^T dG, dW3 = X^T dU                 (one launch)
+//   dw2     dW2 = H^T dY
+// and for the router, with dL [T, E] the logits' gradients:
+//   router dx   dx = sum of a token's rows + dL Wr^T   (gather in the epilogue)
+//   router dw   dWr = x^T dL                           (token chunks as groups)
+//
+// Every product is D[256 x 256] tiles of a CTA pair: CTA r holds the M half r
+// of A and the N half r of B, 64-deep k-blocks of 16 KB each in a ring; the
+// leader issues 256 x 256 x 16 MMAs into two TMEM accumulators in turn.  What
+// differs is which side of an operand is contiguous in memory: tcgen05 takes
+// either from shared memory, so no operand is ever transposed:
+//   K contiguous  (X, dY, dG|dU; W2 and W1, W3 as transposed weights): boxes
+//                 of 64 k x 128 rows;
+//   M or N contiguous (W1, W3, W2 as plain weights; every operand of a weight
+//                 gradient, whose k is the token): two boxes of 64 columns x
+//                 64 k.
+// Out-of-range columns and weight rows are zero-filled by TMA (the weights'
+// maps are 3-D, so a box never reads the next expert).  A weight gradient's
+// k ends inside a box where a group ends: there the rows behind the group
+// (other experts' rows, or memory nobody wrote) are cleared in shared memory,
+// in both operands, before the MMA reads them.
+//
+// Pair protocol: each CTA's loads complete on its own full[]; its warp 1 then
+// tells the leader (ready[], after clearing a group's tail), the leader's
+// warp 1 issues the MMAs and commits empty[] and tfull[] to both CTAs; the
+// epilogue warps of both arrive on the leader's tempty[].  Tiles are dealt
+// round-robin; every role derives them from the offsets.  Every wait is
+// bounded: one that runs out records its code, raises both abort flags, and
+// all roles stop; a CTA's producer then waits for its own copies and the
+// leader for its MMAs before the pair frees TMEM.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <cstring>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBK = 64;
+constexpr int kStages = 6;
+constexpr uint32_t kOperand = 16384u;  // one CTA's half of an operand: 128 x 64 bf16
+constexpr uint32_t kStageBytes = 2 * kOperand;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kMaxGroups = 256;
+constexpr int kRaster = 8;  // tile columns walked together: the operands of the ~74 tiles in flight stay in L2
+
+enum Epi : int { E_GATE, E_F32, E_DGATE, E_BF16, E_GATHER, E_WGRAD };
+
+struct Args {
+    const int32_t* off;  // [G + 1] group offsets, or nullptr: groups of `chunk` rows
+    int64_t cap;         // rows of the token matrices
+    int64_t chunk;
+    int G;
+    int M;             // weight gradients: output rows of a group
+    int N;             // output columns (E_GATE: of each projection)
+    int n_tiles, m_tiles;
+    int kb_first, kb_all;  // k-blocks of the first operand pair, and of both (token-major products)
+    int n_first;           // weight gradients: column tiles of the first output
+    int64_t ld;            // output row stride
+    void* out[2];
+    bf16* h;               // E_GATE: activations out
+    const bf16* gu;        // E_DGATE: saved projections [rows, 2 N]
+    int out_bf16;          // E_GATHER, E_WGRAD
+    const bf16* rows;      // E_GATHER: rows to add, or nullptr
+    const int32_t* inv;
+    int K;
+    int* status;
+    uint32_t wait_limit;
+};
+
+struct Maps {
+    CUtensorMap a[2];
+    CUtensorMap b[2];
+};
+
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+    uint32_t out;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));
+    return out;
+}
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void load_2d(const CUtensorMap* map, uint32_t dst, uint64_t* bar, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void load_3d(const CUtensorMap* map, uint32_t dst, uint64_t* bar, int32_t x, int32_t y,
+                                        int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+
+// Operand whose M or N side is contiguous: two boxes of 64 columns x 64 k
+// (rows of 128 B, 128-byte swizzle), 8 KB apart (leading offset); 8-k groups
+// are 1024 B apart (stride offset).  One MMA covers 16 k: 2048 B.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(8192u >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+struct Tile {
+    int g, n, m;       // group, column tile, row tile
+    int64_t row0;      // token-major: first token row; weight gradient: first row of the reduction
+    int rows;          // token-major: valid rows of the tile (<= 256)
+    int kb;            // k-blocks
+    int k_tail;        // weight gradient: valid rows of the last k-block
+};
+
+struct Sched {
+    const int* off;   // clamped offsets
+    const int* start; // first tile of each group
+    int total;
+};
+
+template <bool WG>
+__device__ __forceinline__ Tile decode(const Args& a, const Sched& sc, int tile) {
+    Tile t;
+    int lo = 0, hi = a.G;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sc.start[mid] <= tile) lo = mid; else hi = mid;
+    }
+    t.g = lo;
+    const int local = tile - sc.start[lo];
+    const int rows = max(0, sc.off[lo + 1] - sc.off[lo]);
+    const int mt = WG ? a.m_tiles : (rows + 255) >> 8;
+    const int band = local / (mt * kRaster);
+    const int width = min(kRaster, a.n_tiles - band * kRaster);
+    const int in = local - band * kRaster * mt;
+    t.m = in / width;
+    t.n = band * kRaster + in - t.m * width;
+    if (WG) {
+        t.row0 = sc.off[lo];
+        t.rows = 256;
+        t.kb = (rows + kBK - 1) / kBK;
+        t.k_tail = rows - (t.kb - 1) * kBK;
+    } else {
+        t.row0 = sc.off[lo] + t.m * 256;
+        t.rows = min(256, rows - t.m * 256);
+        t.kb = a.kb_all;
+        t.k_tail = kBK;
+    }
+    return t;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&p);
+}
+__device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// 8 consecutive values to 16 bytes of bf16 (round to nearest even).
+__device__ __forceinline__ void store8(bf16* dst, const float* v) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* dst, const float* v) {
+    reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// Logistic function with the fast exponential and division: what comes of it
+// is rounded to bf16, whose step is 2^15 times their error.  For x below -88
+// the exponential overflows to infinity and the quotient is 0, its limit.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+// A wait that gives up after a.wait_limit polls; its failure, or an abort
+// seen, stops both CTAs of the pair.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const Args& a, int code,
+                                              volatile int* abort_flag, uint32_t peer_abort) {
+    for (uint32_t i = 0; i < a.wait_limit; ++i) {
+        if (try_wait_cluster(bar, parity)) return true;
+        if ((i & 255u) == 255u) {
+            if (*abort_flag) return false;
+            if (i > 65536u) __nanosleep(64);
+        }
+    }
+    atomicCAS(a.status, 0, code);
+    *abort_flag = 1;
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer_abort), "r"(1) : "memory");
+    return false;
+}
+
+// The same for a whole warp: every lane leaves with the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Args& a, int code,
+                                          volatile int* abort_flag, uint32_t peer_abort) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, a, code, abort_flag, peer_abort)) != 0;
+}
+
+// What the epilogue does with 32 accumulator columns (32-column chunk of the
+// tile at output column `col`) of output row `row`.
+template <int EPI>
+__device__ __forceinline__ void emit(const Args& a, const Tile& t, int64_t row, int col, const float* v, const float* u) {
+    if (EPI == E_GATE) {
+        bf16* gu = static_cast<bf16*>(a.out[0]) + row * a.ld;
+        bf16* h = a.h + row * a.N;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            if (col + j >= a.N) break;
+            float hv[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) hv[i] = v[j + i] * sigmoid(v[j + i]) * u[j + i];
+            store8(gu + col + j, v + j);
+            store8(gu + a.N + col + j, u + j);
+            store8(h + col + j, hv);
+        }
+    } else if (EPI == E_DGATE) {
+        bf16* dgu = static_cast<bf16*>(a.out[0]) + row * a.ld;
+        const bf16* gu = a.gu + row * a.ld;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            if (col + j >= a.N) break;
+            const uint4 gv = *reinterpret_cast<const uint4*>(gu + col + j);
+            const uint4 uv = *reinterpret_cast<const uint4*>(gu + a.N + col + j);
+            const uint32_t gs[4] = {gv.x, gv.y, gv.z, gv.w}, us[4] = {uv.x, uv.y, uv.z, uv.w};
+            float dg[8], du[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float g = (i & 1) ? bf_hi(gs[i >> 1]) : bf_lo(gs[i >> 1]);
+                const float uu = (i & 1) ? bf_hi(us[i >> 1]) : bf_lo(us[i >> 1]);
+                const float s = sigmoid(g);
+                dg[i] = v[j + i] * uu * s * (1.0f + g * (1.0f - s));
+                du[i] = v[j + i] * g * s;
+            }
+            store8(dgu + col + j, dg);
+            store8(dgu + a.N + col + j, du);
+        }
+    } else if (EPI == E_F32) {
+        float* out = static_cast<float*>(a.out[0]) + row * a.ld;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8)
+            if (col + j < a.N) store8(out + col + j, v + j);
+    } else if (EPI == E_BF16) {
+        bf16* out = static_cast<bf16*>(a.out[0]) + row * a.ld;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8)
+            if (col + j < a.N) store8(out + col + j, v + j);
+    } else if (EPI == E_GATHER) {
+        float s[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = v[i];
+        if (a.rows != nullptr)
+            for (int k = 0; k < a.K; ++k) {
+                const int r = a.inv[row * a.K + k];
+                if (static_cast<unsigned>(r) >= static_cast<unsigned>(a.cap * a.K)) continue;  // dropped
+                const bf16* src = a.rows + static_cast<int64_t>(r) * a.ld;
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) {
+                    if (col + j >= a.N) break;
+                    const uint4 q = *reinterpret_cast<const uint4*>(src + col + j);
+                    s[j + 0] += bf_lo(q.x);
+                    s[j + 1] += bf_hi(q.x);
+                    s[j + 2] += bf_lo(q.y);
+                    s[j + 3] += bf_hi(q.y);
+                    s[j + 4] += bf_lo(q.z);
+                    s[j + 5] += bf_hi(q.z);
+                    s[j + 6] += bf_lo(q.w);
+                    s[j + 7] += bf_hi(q.w);
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            if (col + j >= a.N) break;
+            if (a.out_bf16) store8(static_cast<bf16*>(a.out[0]) + row * a.ld + col + j, s + j);
+            else store8(static_cast<float*>(a.out[0]) + row * a.ld + col + j, s + j);
+        }
+    } else {  // E_WGRAD
+        const int sel = t.n >= a.n_first ? 1 : 0;
+        const int64_t at = (static_cast<int64_t>(t.g) * a.M + row) * a.ld;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            if (col + j >= a.N) break;
+            if (a.out_bf16) store8(static_cast<bf16*>(a.out[sel]) + at + col + j, v + j);
+            else store8(static_cast<float*>(a.out[sel]) + at + col + j, v + j);
+        }
+    }
+}
+
+template <int EPI, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
+    constexpr bool WG = EPI == E_WGRAD;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    uint64_t* empty = full + kStages;
+    uint64_t* ready = empty + kStages;
+    uint64_t* tfull = ready + kStages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* off = reinterpret_cast<int*>(tmem_slot + 2);
+    int* start = off + kMaxGroups + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&ready[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 2 * kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        for (int i = 0; i < 2; ++i) {
+            tma_prefetch_desc(&maps.a[i]);
+            tma_prefetch_desc(&maps.b[i]);
+        }
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    // Offsets clamped to the matrices' rows: no value in the array is ever an address.
+    for (int g = threadIdx.x; g <= a.G; g += kThreads) {
+        const int64_t o = a.off != nullptr ? static_cast<int64_t>(a.off[g]) : static_cast<int64_t>(g) * a.chunk;
+        off[g] = static_cast<int>(o < 0 ? 0 : (o > a.cap ? a.cap : o));
+    }
+    __syncthreads();
+    if (warp == 0) {  // a group whose end lies before its start is empty
+        int carry = 0;
+        for (int g0 = 0; g0 < a.G; g0 += 32) {
+            const int g = g0 + lane;
+            const int rows = g < a.G ? max(0, off[g + 1] - off[g]) : 0;
+            const int n = g < a.G ? (WG ? a.m_tiles : (rows + 255) >> 8) * a.n_tiles : 0;
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (g < a.G) start[g] = carry + incl - n;
+            carry += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) start[a.G] = carry;
+    }
+    tc_fence_before();
+    __syncthreads();
+    pair_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const Sched sc{off, start, start[a.G]};
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const uint32_t peer_abort = peer_addr(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ producer (both CTAs)
+            uint32_t s = 0, ph = 0, uses = 0;
+            bool ok = true;
+            for (int tile = pair; ok && tile < sc.total; tile += npairs) {
+                const Tile t = decode<WG>(a, sc, tile);
+                const int sel = WG && t.n >= a.n_first ? 1 : 0;
+                const int n0 = WG ? (t.n - sel * a.n_first) * 256 + 128 * static_cast<int>(rank)
+                                  : (EPI == E_GATE ? t.n * 128 : t.n * 256 + 128 * static_cast<int>(rank));
+                for (int kb = 0; kb < t.kb; ++kb) {
+                    if (!wait_or_abort(&empty[s], ph ^ 1u, a, DEV_TIMEOUT_PRODUCER_EMPTY, abort_flag, peer_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&full[s], kStageBytes);
+                    const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kOperand;
+                    if (WG) {
+                        const int y = static_cast<int>(t.row0) + kb * kBK;
+                        const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
+                        load_2d(&maps.a[0], sa, &full[s], m0, y);
+                        load_2d(&maps.a[0], sa + 8192, &full[s], m0 + 64, y);
+                        load_2d(&maps.b[sel], sb, &full[s], n0, y);
+                        load_2d(&maps.b[sel], sb + 8192, &full[s], n0 + 64, y);
+                    } else {
+                        const int second = kb >= a.kb_first ? 1 : 0;
+                        const int k0 = (kb - (second ? a.kb_first : 0)) * kBK;
+                        load_2d(&maps.a[second], sa, &full[s], k0, static_cast<int>(t.row0) + 128 * static_cast<int>(rank));
+                        const CUtensorMap* b = EPI == E_GATE ? &maps.b[rank] : &maps.b[second];
+                        if (B_MN) {
+                            load_3d(b, sb, &full[s], n0, k0, t.g);
+                            load_3d(b, sb + 8192, &full[s], n0 + 64, k0, t.g);
+                        } else {
+                            load_3d(b, sb, &full[s], k0, n0, t.g);
+                        }
+                    }
+                    ++uses;
+                    if (++s == kStages) { s = 0; ph ^= 1u; }
+                }
+            }
+            // every copy of this CTA has landed before it can exit
+            const uint32_t first = uses > kStages ? uses - kStages : 0u;
+            for (uint32_t u = first; u < uses; ++u)
+                mbar_drain(&full[u % kStages], (u / kStages) & 1u, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer (leader), its helper (peer)
+        // idesc: D fp32, A and B bf16, bits 15 and 16 set where A, B are M-, N-contiguous
+        constexpr uint32_t idesc = umma_idesc_bf16(256, 256) | (WG ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
+        const uint32_t leader_ready = peer_addr(smem_u32(ready), 0);
+        uint32_t s = 0, ph = 0;
+        int it = 0;
+        bool ok = true;
+        for (int tile = pair; ok && tile < sc.total; tile += npairs) {
+            const Tile t = decode<WG>(a, sc, tile);
+            if (t.kb == 0) continue;
+            const int buf = it & 1;
+            const uint32_t use = static_cast<uint32_t>(it >> 1);
+            ++it;
+            if (leader) {
+                if (!warp_wait(&tempty[buf], (use & 1u) ^ 1u, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
+                tc_fence_after();
+            }
+            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf) * 256u;
+            for (int kb = 0; kb < t.kb; ++kb) {
+                if (!warp_wait(&full[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t stage = smem_u32(smem + s * kStageBytes);
+                int steps = kBK / 16;
+                if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
+                    // the group ends inside this box: clear the rows behind it up
+                    // to the last 16-row step that is multiplied
+                    steps = (t.k_tail + 15) / 16;
+                    const int from = t.k_tail * 8, to = steps * 16 * 8;  // 16-byte units of a 64-column box
+                    uint4* box = reinterpret_cast<uint4*>(smem + s * kStageBytes);
+                    for (int i = from + lane; i < to; i += 32)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) box[b * 512 + i] = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (!leader) {
+                    if (lane == 0) arrive_cluster(leader_ready + 8u * s);
+                } else {
+                    if (!warp_wait(&ready[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; ++kk) {
+                            if (WG && kk >= steps) break;
+                            const uint64_t da = WG ? desc_mn(stage + kk * 2048) : umma_desc_sw128(stage + kk * 32);
+                            const uint64_t db = B_MN ? desc_mn(stage + kOperand + kk * 2048) : umma_desc_sw128(stage + kOperand + kk * 32);
+                            mma_pair(d_tmem, da, db, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        commit_pair(&empty[s]);
+                        if (kb == t.kb - 1) commit_pair(&tfull[buf]);
+                    }
+                    __syncwarp();
+                }
+                if (++s == kStages) { s = 0; ph ^= 1u; }
+            }
+        }
+        if (leader && lane == 0) {  // every MMA issued is complete before TMEM is freed
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                         ::"r"(smem_u32(drain)) : "memory");
+            mbar_drain(drain, 0, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------- epilogue (both CTAs)
+        // Warp quarter q holds rows 32 q .. of this CTA's 128; the two warps of
+        // a quarter take the two column halves.
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t leader_tempty = peer_addr(smem_u32(tempty), 0);
+        int it = 0;
+        for (int tile = pair; tile < sc.total; tile += npairs) {
+            const Tile t = decode<WG>(a, sc, tile);
+            const int r = static_cast<int>(rank) * 128 + q * 32 + lane;  // row of the tile
+            const bool valid = WG ? t.m * 256 + r < a.M : r < t.rows;
+            const int64_t row = WG ? t.m * 256 + r : t.row0 + r;
+            const int sel = WG && t.n >= a.n_first ? 1 : 0;
+            const int col0 = (t.n - sel * a.n_first) * (EPI == E_GATE ? 128 : 256) + half * (EPI == E_GATE ? 64 : 128);
+            float v[32], u[32];
+            if (WG && t.kb == 0) {  // no rows: the gradient is zero
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                for (int c = 0; c < 4; ++c)
+                    if (valid) emit<EPI>(a, t, row, col0 + 32 * c, v, u);
+                continue;
+            }
+            const int buf = it & 1;
+            const uint32_t use = static_cast<uint32_t>(it >> 1);
+            ++it;
+            if (!warp_wait(&tfull[buf], use & 1u, a, DEV_TIMEOUT_EPI_TFULL, abort_flag, peer_abort)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + static_cast<uint32_t>(buf) * 256u + (static_cast<uint32_t>(q * 32) << 16);
+            if (EPI == E_GATE) {
+                for (int c = 0; c < 2; ++c) {
+                    tmem_ld32(taddr + static_cast<uint32_t>(half * 64 + c * 32), v);
+                    tmem_ld32(taddr + static_cast<uint32_t>(128 + half * 64 + c * 32), u);
+                    if (valid) emit<EPI>(a, t, row, col0 + 32 * c, v, u);
+                    __syncwarp();
+                }
+            } else {
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld32(taddr + static_cast<uint32_t>(half * 128 + c * 32), v);
+                    if (valid) emit<EPI>(a, t, row, col0 + 32 * c, v, u);
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(leader_tempty + 8u * buf);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    pair_sync();  // neither CTA's memory goes while the other may still use it
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// bf16 matrix [rows, cols] with row stride ld (elements), boxes of 64 columns x box_rows.
+bool map_matrix(CUtensorMap* m, const bf16* base, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows) {
+    auto enc = map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows < 1 ? 1 : rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    cuuint32_t box[2] = {64u, box_rows}, es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// bf16 matrices [mats, rows, cols], boxes of 64 columns x box_rows of one matrix.
+bool map_weights(CUtensorMap* m, const bf16* base, int64_t mats, int64_t rows, int64_t cols, uint32_t box_rows) {
+    auto enc = map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(mats)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(rows) * cols * 2};
+    cuuint32_t box[3] = {64u, box_rows, 1u}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + (3 * kStages + 5) * 8 + 8 + 2 * (kMaxGroups + 1) * 4;
+
+template <int EPI, bool B_MN>
+int launch(const Maps& maps, Args a, int max_pairs, cudaStream_t st) {
+    static std::atomic<unsigned long long> attr_done{0};
+    if (a.G < 1 || a.G > kMaxGroups) return -2;
+    const auto kernel = train_gemm_kernel<EPI, B_MN>;
+    if (smem_attr_once(reinterpret_cast<const void*>(kernel), static_cast<int>(kSmem), attr_done) != 0) return -3;
+    const uint32_t limit = wait_settings().wait_limit;
+    a.wait_limit = limit ? limit : kWaitLimit;
+    int pairs = num_sms() / 2;
+    if (pairs < 1) return -3;
+    if (pairs > max_pairs) pairs = max_pairs;
+    kernel<<<2 * pairs, kThreads, kSmem, st>>>(maps, a);
+    return cudaGetLastError() == cudaSuccess ? 0 : -3;
+}
+
+// Upper bound of a token-major launch's tiles: a group's last tile may be partial.
+int tile_bound(int64_t rows, int G, int n_tiles) {
+    const int64_t t = ((rows + 255) / 256 + G) * n_tiles;
+    return t > (1 << 20) ? (1 << 20) : static_cast<int>(t);
+}
+
+}  // namespace
+
+int launch_train_gate(const bf16* x, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W1,
+                      const bf16* W3, bf16* gu, bf16* h, int* status, cudaStream_t st) {
+    Maps m;
+    std::memset(&m, 0, sizeof(m));
+    if (!map_matrix(&m.a[0], x, rows, d, d, 128) || !map_weights(&m.b[0], W1, E, d, f, 64) ||
+        !map_weights(&m.b[1], W3, E, d, f, 64))
+        return -3;
+    m.a[1] = m.a[0];
+    Args a{};
+    a.off = off;
+    a.cap = rows;
+    a.G = E;
+    a.N = f;
+    a.n_tiles = ceil_div(f, 128);
+    a.kb_first = a.kb_all = ceil_div(d, kBK);
+    a.ld = 2 * static_cast<int64_t>(f);
+    a.out[0] = gu;
+    a.h = h;
+    a.status = status;
+    return launch<E_GATE, true>(m, a, tile_bound(rows, E, a.n_tiles), st);
+}
+
+int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2, float* y,
+                      int* status, cudaStream_t st) {
+    Maps m;
+    std::memset(&m, 0, sizeof(m));
+    if (!map_matrix(&m.a[0], h, rows, f, f, 128) || !map_weights(&m.b[0], W2, E, f, d, 64)) return -3;
+    m.a[1] = m.a[0];
+    m.b[1] = m.b[0];
+    Args a{};
+    a.off = off;
+    a.cap = rows;
+    a.G = E;
+    a.N = d;
+    a.n_tiles = ceil_div(d, 256);
+    a.kb_first = a.kb_all = ceil_div(f, kBK);
+    a.ld = d;
+    a.out[0] = y;
+    a.status = status;
+    return launch<E_F32, true>(m, a, tile_bound(rows, E, a.n_tiles), st);
+}
+
+int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2,
+                       const bf16* gu, bf16* dgu, int* status, cudaStream_t st) {
+    Maps m;
+    std::memset(&m, 0, sizeof(m));
+    if (!map_matrix(&m.a[0], dy, rows, d, d, 128) || !map_weights(&m.b[0], W2, E, f, d, 128)) return -3;
+    m.a[1] = m.a[0];
+    m.b[1] = m.b[0];
+    Args a{};
+    a.off = off;
+    a.cap = rows;
+    a.G = E;
+    a.N = f;
+    a.n_tiles = ceil_div(f, 256);
+    a.kb_first = a.kb_all = ceil_div(d, kBK);
+    a.ld = 2 * static_cast<int64_t>(f);
+    a.out[0] = dgu;
+    a.gu = gu;
+    a.status = status;
+    return launch<E_DGATE, false>(m, a, tile_bound(rows, E, a.n_tiles), st);
+}
+
+int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W1,
+                    const bf16* W3, bf16* dx, int* status, cudaStream_t st) {
+    Maps m;
+    std::memset(&m, 0, sizeof(m));
+    const int64_t ld = 2 * static_cast<int64_t>(f);
+    if (!map_matrix(&m.a[0], dgu, rows, f, ld, 128) || !map_matrix(&m.a[1], dgu + f, rows, f, ld, 128) ||
+        !map_weights(&m.b[0], W1, E, d, f, 128) || !map_weights(&m.b[1], W3, E, d, f, 128))
+        return -3;
+    Args a{};
+    a.off = off;
+    a.cap = rows;
+    a.G = E;
+    a.N = d;
+    a.n_tiles = ceil_div(d, 256);
+    a.kb_first = ceil_div(f, kBK);
+    a.kb_all = 2 * a.kb_first;
+    a.ld = d;
+    a.out[0] = dx;
+    a.status = status;
+    return launch<E_BF16, false>(m, a, tile_bound(rows, E, a.n_tiles), st);
+}
+
+int launch_train_dw(const bf16* left, int m_cols, const bf16* right0, const bf16* right1, int64_t right_ld, int n_cols,
+                    const int32_t* off, int64_t chunk, int64_t rows, int G, void* out0, void* out1, int64_t out_ld,
+                    bool out_bf16, int* status, cudaStream_t st) {
+    Maps m;
+    std::memset(&m, 0, sizeof(m));
+    if (!map_matrix(&m.a[0], left, rows, m_cols, m_cols, 64) || !map_matrix(&m.b[0], right0, rows, n_cols, right_ld, 64))
+        return -3;
+    m.a[1] = m.a[0];
+    m.b[1] = m.b[0];
+    if (right1 && !map_matrix(&m.b[1], right1, rows, n_cols, right_ld, 64)) return -3;
+    Args a{};
+    a.off = off;
+    a.chunk = chunk;
+    a.cap = rows;
+    a.G = G;
+    a.M = m_cols;
+    a.N = n_cols;
+    a.m_tiles = ceil_div(m_cols, 256);
+    a.n_first = ceil_div(n_cols, 256);
+    a.n_tiles = (right1 ? 2 : 1) * a.n_first;
+    a.ld = out_ld;
+    a.out[0] = out0;
+    a.out[1] = out1;
+    a.out_bf16 = out_bf16 ? 1 : 0;
+    a.status = status;
+    const int64_t tiles = static_cast<int64_t>(G) * a.m_tiles * a.n_tiles;
+    return launch<E_WGRAD, true>(m, a, tiles > (1 << 20) ? (1 << 20) : static_cast<int>(tiles), st);
+}
+
+int launch_train_router_dx(const bf16* dl, int64_t T, int dl_ld, const bf16* Wr, int wr_ld, int E, int d, const bf16* rows,
+                           const int32_t* inv, int K, void* dx, bool dx_bf16, int* status, cudaStream_t st) {
+    Maps m;
+    std::memset(&m, 0, sizeof(m));
+    if (!map_matrix(&m.a[0], dl, T, E, dl_ld, 128) || !map_weights(&m.b[0], Wr, 1, d, wr_ld, 128)) return -3;
+    m.a[1] = m.a[0];
+    m.b[1] = m.b[0];
+    Args a{};
+    a.off = nullptr;
+    a.chunk = T;
+    a.cap = T;
+    a.G = 1;
+    a.N = d;
+    a.n_tiles = ceil_div(d, 256);
+    a.kb_first = a.kb_all = ceil_div(E, kBK);
+    a.ld = d;
+    a.out[0] = dx;
+    a.out_bf16 = dx_bf16 ? 1 : 0;
+    a.rows = rows;
+    a.inv = inv;
+    a.K = K;
+    a.status = status;
+    return launch<E_GATHER, false>(m, a, tile_bound(T, 1, a.n_tiles), st);
+}
+
+}  // namespace moe
