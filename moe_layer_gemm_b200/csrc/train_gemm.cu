@@ -30,14 +30,24 @@
 // (other experts' rows, or memory nobody wrote) are cleared in shared memory,
 // in both operands, before the MMA reads them.
 //
-// Pair protocol: each CTA's loads complete on its own full[]; its warp 1 then
-// tells the leader (ready[], after clearing a group's tail), the leader's
-// warp 1 issues the MMAs and commits empty[] and tfull[] to both CTAs; the
-// epilogue warps of both arrive on the leader's tempty[].  Tiles are dealt
-// round-robin; every role derives them from the offsets.  Every wait is
-// bounded: one that runs out records its code, raises both abort flags, and
-// all roles stop; a CTA's producer then waits for its own copies and the
-// leader for its MMAs before the pair frees TMEM.
+// Pair protocol (each CTA has every barrier; "leader" is rank 0's copy):
+//   full[s]    leader: armed for the pair's bytes, both CTAs' loads complete on it
+//   empty[s]   both: the leader's MMA commit arrives on both
+//   tfull[b]   both: the leader's MMA commit arrives on both
+//   tempty[b]  leader: all epilogue warps of the pair arrive
+//   tail[s]    both: a CTA's own loads of a k-block that its group ends in
+//   clear[s]   leader: the peer has cleared the rows behind the group
+// Only full[] and empty[] are used per k-block, and nothing a k-block waits
+// for goes through the peer's threads: with each CTA's loads on its own full[]
+// and a thread of the peer passing the news on, a release-arrive a k-block
+// across the pair cost 1.15 us, a relaxed one 0.53 us.
+// Tiles are dealt round-robin; every role derives them from the offsets.
+// Every wait is bounded: one that runs out records its code and raises both
+// abort flags, and all roles of the pair stop.  Then, as after a complete run,
+// the two producers' counts are compared: the leader completes by hand the
+// bytes of the peer's loads that it armed and the peer never issued, arms
+// those that the peer issued ahead of it, and waits for all of them and for
+// its MMAs before the pair frees TMEM.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -102,9 +112,13 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void pair_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void store_cluster(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// Acquire at cluster scope: for arrivals that publish the other CTA's writes.
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\t"
@@ -113,14 +127,17 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
                  : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ void load_2d(const CUtensorMap* map, uint32_t dst, uint64_t* bar, int32_t x, int32_t y) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+// Loads into this CTA's shared memory that complete on a barrier of either CTA.
+__device__ __forceinline__ void load_2d(const CUtensorMap* map, uint32_t dst, uint32_t bar, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void load_3d(const CUtensorMap* map, uint32_t dst, uint64_t* bar, int32_t x, int32_t y,
+__device__ __forceinline__ void load_3d(const CUtensorMap* map, uint32_t dst, uint32_t bar, int32_t x, int32_t y,
                                         int32_t z) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -213,10 +230,11 @@ __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f
 
 // A wait that gives up after a.wait_limit polls; its failure, or an abort
 // seen, stops both CTAs of the pair.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const Args& a, int code,
                                               volatile int* abort_flag, uint32_t peer_abort) {
     for (uint32_t i = 0; i < a.wait_limit; ++i) {
-        if (try_wait_cluster(bar, parity)) return true;
+        if (CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if ((i & 255u) == 255u) {
             if (*abort_flag) return false;
             if (i > 65536u) __nanosleep(64);
@@ -224,14 +242,15 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, co
     }
     atomicCAS(a.status, 0, code);
     *abort_flag = 1;
-    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer_abort), "r"(1) : "memory");
+    store_cluster(peer_abort, 1u);
     return false;
 }
 
 // The same for a whole warp: every lane leaves with the same answer.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Args& a, int code,
                                           volatile int* abort_flag, uint32_t peer_abort) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, a, code, abort_flag, peer_abort)) != 0;
+    return __all_sync(0xffffffffu, wait_or_abort<CLUSTER>(bar, parity, a, code, abort_flag, peer_abort)) != 0;
 }
 
 // What the epilogue does with 32 accumulator columns (32-column chunk of the
@@ -331,13 +350,15 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
     uint64_t* empty = full + kStages;
-    uint64_t* ready = empty + kStages;
-    uint64_t* tfull = ready + kStages;
+    uint64_t* tail = empty + kStages;
+    uint64_t* clear = tail + kStages;
+    uint64_t* tfull = clear + kStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* off = reinterpret_cast<int*>(tmem_slot + 2);
+    uint32_t* issued = tmem_slot + 2;  // [rank][stage uses issued, which stages' last use was a tail]
+    int* off = reinterpret_cast<int*>(tmem_slot + 6);
     int* start = off + kMaxGroups + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -347,7 +368,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-            mbar_init(&ready[s], 1);
+            mbar_init(&tail[s], 1);
+            mbar_init(&clear[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
@@ -401,7 +423,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     if (warp == 0) {
         if (lane == 0) {
             // ------------------------------------------------ producer (both CTAs)
-            uint32_t s = 0, ph = 0, uses = 0;
+            const uint32_t leader_full = peer_addr(smem_u32(full), 0), own_tail = peer_addr(smem_u32(tail), rank);
+            uint32_t s = 0, ph = 0, uses = 0, tails = 0, tail_ph = 0;
             bool ok = true;
             for (int tile = pair; ok && tile < sc.total; tile += npairs) {
                 const Tile t = decode<WG>(a, sc, tile);
@@ -413,65 +436,79 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[s], kStageBytes);
                     const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kOperand;
+                    uint32_t bar = leader_full + 8u * s;
+                    if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
+                        bar = own_tail + 8u * s;
+                        mbar_arrive_expect_tx(&tail[s], kStageBytes);
+                        if (leader) mbar_arrive(&full[s]);
+                        tails |= 1u << s;
+                        tail_ph ^= 1u << s;
+                    } else {
+                        if (leader) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                        tails &= ~(1u << s);
+                    }
                     if (WG) {
                         const int y = static_cast<int>(t.row0) + kb * kBK;
                         const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
-                        load_2d(&maps.a[0], sa, &full[s], m0, y);
-                        load_2d(&maps.a[0], sa + 8192, &full[s], m0 + 64, y);
-                        load_2d(&maps.b[sel], sb, &full[s], n0, y);
-                        load_2d(&maps.b[sel], sb + 8192, &full[s], n0 + 64, y);
+                        load_2d(&maps.a[0], sa, bar, m0, y);
+                        load_2d(&maps.a[0], sa + 8192, bar, m0 + 64, y);
+                        load_2d(&maps.b[sel], sb, bar, n0, y);
+                        load_2d(&maps.b[sel], sb + 8192, bar, n0 + 64, y);
                     } else {
                         const int second = kb >= a.kb_first ? 1 : 0;
                         const int k0 = (kb - (second ? a.kb_first : 0)) * kBK;
-                        load_2d(&maps.a[second], sa, &full[s], k0, static_cast<int>(t.row0) + 128 * static_cast<int>(rank));
+                        load_2d(&maps.a[second], sa, bar, k0, static_cast<int>(t.row0) + 128 * static_cast<int>(rank));
                         const CUtensorMap* b = EPI == E_GATE ? &maps.b[rank] : &maps.b[second];
                         if (B_MN) {
-                            load_3d(b, sb, &full[s], n0, k0, t.g);
-                            load_3d(b, sb + 8192, &full[s], n0 + 64, k0, t.g);
+                            load_3d(b, sb, bar, n0, k0, t.g);
+                            load_3d(b, sb + 8192, bar, n0 + 64, k0, t.g);
                         } else {
-                            load_3d(b, sb, &full[s], k0, n0, t.g);
+                            load_3d(b, sb, bar, k0, n0, t.g);
                         }
                     }
                     ++uses;
                     if (++s == kStages) { s = 0; ph ^= 1u; }
                 }
             }
-            // every copy of this CTA has landed before it can exit
-            const uint32_t first = uses > kStages ? uses - kStages : 0u;
-            for (uint32_t u = first; u < uses; ++u)
-                mbar_drain(&full[u % kStages], (u / kStages) & 1u, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
+            // this CTA's own tails have landed (a phase never used counts as complete)
+            for (int i = 0; WG && i < kStages; ++i)
+                mbar_drain(&tail[i], ((tail_ph >> i) & 1u) ^ 1u, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
+            const uint32_t rec = peer_addr(smem_u32(issued + 2 * rank), 0);
+            store_cluster(rec, uses);
+            store_cluster(rec + 4, tails);
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer (leader), its helper (peer)
+        // ---------------------------------------------------- MMA issuer (leader); the peer only clears tails
         // idesc: D fp32, A and B bf16, bits 15 and 16 set where A, B are M-, N-contiguous
         constexpr uint32_t idesc = umma_idesc_bf16(256, 256) | (WG ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
-        const uint32_t leader_ready = peer_addr(smem_u32(ready), 0);
-        uint32_t s = 0, ph = 0;
+        const uint32_t leader_clear = peer_addr(smem_u32(clear), 0);
+        uint32_t s = 0, ph = 0, tail_ph = 0;
         int it = 0;
         bool ok = true;
-        for (int tile = pair; ok && tile < sc.total; tile += npairs) {
+        for (int tile = pair; ok && (WG || leader) && tile < sc.total; tile += npairs) {
             const Tile t = decode<WG>(a, sc, tile);
             if (t.kb == 0) continue;
             const int buf = it & 1;
             const uint32_t use = static_cast<uint32_t>(it >> 1);
             ++it;
             if (leader) {
-                if (!warp_wait(&tempty[buf], (use & 1u) ^ 1u, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
+                if (!warp_wait<true>(&tempty[buf], (use & 1u) ^ 1u, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
                 tc_fence_after();
             }
             const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf) * 256u;
             for (int kb = 0; kb < t.kb; ++kb) {
-                if (!warp_wait(&full[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
-                    ok = false;
-                    break;
-                }
                 const uint32_t stage = smem_u32(smem + s * kStageBytes);
                 int steps = kBK / 16;
                 if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
                     // the group ends inside this box: clear the rows behind it up
                     // to the last 16-row step that is multiplied
+                    const uint32_t tph = (tail_ph >> s) & 1u;
+                    tail_ph ^= 1u << s;
+                    if (!warp_wait(&tail[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
+                        ok = false;
+                        break;
+                    }
                     steps = (t.k_tail + 15) / 16;
                     const int from = t.k_tail * 8, to = steps * 16 * 8;  // 16-byte units of a 64-column box
                     uint4* box = reinterpret_cast<uint4*>(smem + s * kStageBytes);
@@ -479,12 +516,16 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
 #pragma unroll
                         for (int b = 0; b < 4; ++b) box[b * 512 + i] = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
+                    __syncwarp();
+                    if (!leader) {
+                        if (lane == 0) arrive_cluster(leader_clear + 8u * s);
+                    } else if (!warp_wait<true>(&clear[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
+                        ok = false;
+                        break;
+                    }
                 }
-                __syncwarp();
-                if (!leader) {
-                    if (lane == 0) arrive_cluster(leader_ready + 8u * s);
-                } else {
-                    if (!warp_wait(&ready[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
+                if (leader) {
+                    if (!warp_wait(&full[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
                         ok = false;
                         break;
                     }
@@ -561,6 +602,24 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
 
     tc_fence_before();
     __syncthreads();
+    pair_sync();  // all roles of both CTAs have stopped
+    if (leader && threadIdx.x == 0) {
+        // No copy is in flight when the pair ends.  A complete run issued the
+        // same uses on both sides; after an abort the leader makes up for the
+        // difference (at most the ring, since a use waits for its stage).
+        const uint32_t mine = issued[0], theirs = issued[2];
+        const uint32_t first = mine > kStages ? mine - kStages : 0u;
+        for (uint32_t u = theirs > first ? theirs : first; u < mine; ++u)
+            if (!((issued[1] >> (u % kStages)) & 1u)) mbar_complete_tx(&full[u % kStages], kStageBytes);
+        for (uint32_t u = mine; u < theirs && u < mine + kStages; ++u) {
+            if ((issued[3] >> (u % kStages)) & 1u) mbar_arrive(&full[u % kStages]);
+            else mbar_arrive_expect_tx(&full[u % kStages], kStageBytes);
+        }
+        const uint32_t last = theirs > mine ? theirs : mine;
+        for (uint32_t u = last > kStages ? last - kStages : 0u; u < last; ++u)
+            mbar_drain(&full[u % kStages], (u / kStages) & 1u, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
+    }
+    __syncthreads();
     pair_sync();  // neither CTA's memory goes while the other may still use it
     if (warp == 1) {
         tc_fence_after();
@@ -605,7 +664,7 @@ bool map_weights(CUtensorMap* m, const bf16* base, int64_t mats, int64_t rows, i
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-constexpr size_t kSmem = 1024 + kStages * kStageBytes + (3 * kStages + 5) * 8 + 8 + 2 * (kMaxGroups + 1) * 4;
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + (4 * kStages + 5) * 8 + 24 + 2 * (kMaxGroups + 1) * 4;
 
 template <int EPI, bool B_MN>
 int launch(const Maps& maps, Args a, int max_pairs, cudaStream_t st) {
