@@ -236,9 +236,6 @@ int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, in
 int launch_train_dw(const bf16* left, int m_cols, const bf16* right0, const bf16* right1, int64_t right_ld, int n_cols,
                     const int32_t* off, int64_t chunk, int64_t rows, int G, void* out0, void* out1, int64_t out_ld,
                     bool out_bf16, int* status, cudaStream_t st);
-// dx[t] = dl[t] Wr^T + the sum of token t's rows (rows may be nullptr).
-int launch_train_router_dx(const bf16* dl, int64_t T, int dl_ld, const bf16* Wr, int wr_ld, int E, int d, const bf16* rows,
-                           const int32_t* inv, int K, void* dx, bool dx_bf16, int* status, cudaStream_t st);
 
 // ------------------------------------------------------------ training: around the experts (train.cu)
 int launch_combine_backward(const void* dy, bool dy_bf16, const float* y_perm, const int32_t* inv, const float* w, int64_t T,
@@ -247,6 +244,9 @@ int launch_permute_backward(const bf16* dx_perm, const int32_t* inv, int64_t T, 
                             cudaStream_t st);
 int launch_route_backward(const float* logits, const int32_t* idx, const float* w, const float* dw, const int32_t* counts,
                           float aux, float zc, int64_t T, int E, int K, int ld, float* dlogits, bf16* dl16, cudaStream_t st);
+// dx[t] = dl[t] Wr^T + the sum of token t's rows (dx_perm may be nullptr); dl and Wr have rows of ld elements.
+int launch_router_dx(const bf16* dl, const bf16* Wr, int ld, const bf16* dx_perm, const int32_t* inv, int64_t T, int d, int K,
+                     void* dx, bool dx_bf16, cudaStream_t st);
 int launch_pad_router(const bf16* Wr, int d, int E, int ld, bf16* out, cudaStream_t st);
 int launch_router_weight(const float* part, int S, int d, int E, int ld, void* out, bool out_bf16, cudaStream_t st);
 

@@ -147,8 +147,120 @@ route_backward_kernel(const float* __restrict__ logits, const int32_t* __restric
     }
 }
 
-// Router weight [d, E] with rows of ld elements (TMA reads rows of a multiple
-// of 16 bytes); columns E.. are zero.
+// dx = dl Wr^T + the tokens' rows.  The product has at most 256 terms and the
+// rows' bytes bound the kernel, so it is built as a gather that needs many loads
+// in flight: blocks of 32 tokens x 256 columns, several to an SM, multiply
+// with warp-level MMAs (16 x 8 x 16; each warp 32 tokens x 32 columns), turn
+// the sums round in shared memory and then walk rows, a warp reading 512
+// consecutive bytes.  (The same sum in the epilogue of the CTA-pair GEMM, whose
+// 8 epilogue warps an SM are too few to cover the rows' latency, took 224 us
+// at T = 16384, d = 4096, K = 2.)
+constexpr int kDxTokens = 32, kDxCols = 256, kDxK = 64;
+constexpr int kDxStride = kDxK + 8;   // bf16 operands: rows 16 bytes apart modulo 128
+constexpr int kDxOut = kDxCols + 4;   // fp32 sums
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const bf16* p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))));
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <typename X>
+__global__ void __launch_bounds__(256, 4)
+router_dx_kernel(const bf16* __restrict__ dl, const bf16* __restrict__ Wr, int ld, const bf16* __restrict__ dx_perm,
+                 const int32_t* __restrict__ inv, int64_t T, int d, int K, X* __restrict__ dx) {
+    __shared__ __align__(16) uint8_t smem[(kDxTokens + kDxCols) * kDxStride * 2];
+    bf16* sa = reinterpret_cast<bf16*>(smem);
+    bf16* sb = sa + kDxTokens * kDxStride;
+    float* out = reinterpret_cast<float*>(smem);  // after the product
+    static_assert(sizeof(smem) >= kDxTokens * kDxOut * 4, "the sums fit where the operands were");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kDxTokens;
+    const int n0 = blockIdx.y * kDxCols;
+    float acc[2][4][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    for (int k0 = 0; k0 < ld; k0 += kDxK) {
+        const int width = min(kDxK, (ld - k0 + 15) / 16 * 16) / 8;  // 16-byte units of a row, whole MMA steps
+        if (k0) __syncthreads();
+        for (int i = threadIdx.x; i < (kDxTokens + kDxCols) * width; i += 256) {
+            const int r = i / width, c = (i - r * width) * 8;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (k0 + c < ld) {
+                if (r < kDxTokens) {
+                    if (t0 + r < T) v = *reinterpret_cast<const uint4*>(dl + (t0 + r) * ld + k0 + c);
+                } else if (n0 + r - kDxTokens < d) {
+                    v = *reinterpret_cast<const uint4*>(Wr + static_cast<int64_t>(n0 + r - kDxTokens) * ld + k0 + c);
+                }
+            }
+            *reinterpret_cast<uint4*>(sa + r * kDxStride + c) = v;
+        }
+        __syncthreads();
+        for (int k = 0; k < width * 8; k += 16) {
+            uint32_t a[2][4], b[2][4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) ldmatrix4(a[m], sa + (16 * m + (lane & 15)) * kDxStride + k + 8 * (lane >> 4));
+#pragma unroll
+            for (int n = 0; n < 2; ++n)  // 16 columns: both 8-column halves of k 0-7, then of k 8-15
+                ldmatrix4(b[n], sb + (32 * warp + 16 * n + (lane & 15)) * kDxStride + k + 8 * (lane >> 4));
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) mma_16816(acc[m][n], a[m], b[n >> 1][n & 1], b[n >> 1][2 + (n & 1)]);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2*>(out + (16 * m + 8 * h + (lane >> 2)) * kDxOut + 32 * warp + 8 * n + 2 * (lane & 3)) =
+                    make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+    __syncthreads();
+    // rows warp, warp + 8, ...: the slot's row is the same for the whole warp
+    const int c = n0 + 8 * lane;
+    if (c >= d) return;
+    float s[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load8(out + (warp + 8 * i) * kDxOut + 8 * lane, s[i]);
+    if (dx_perm) {
+        const int64_t rows = T * K;
+        for (int k = 0; k < K; ++k) {
+            int64_t src[4];
+            float v[4][8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t t = t0 + warp + 8 * i;
+                src[i] = inv[(t < T ? t : T - 1) * K + k];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) load8(dx_perm + (src[i] >= 0 && src[i] < rows ? src[i] : 0) * d + c, v[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) s[i][x] += src[i] >= 0 && src[i] < rows ? v[i][x] : 0.f;  // a dropped slot adds nothing
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t t = t0 + warp + 8 * i;
+        if (t < T) put8(dx + t * d + c, s[i]);
+    }
+}
+
+// Router weight [d, E] with rows of ld elements, a multiple of 16 bytes;
+// columns E.. are zero.
 __global__ void __launch_bounds__(256)
 pad_router_kernel(const bf16* __restrict__ Wr, int64_t n, int E, int ld, bf16* __restrict__ out) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -202,6 +314,14 @@ int launch_permute_backward(const bf16* dx_perm, const int32_t* inv, int64_t T, 
 int launch_route_backward(const float* logits, const int32_t* idx, const float* w, const float* dw, const int32_t* counts,
                           float aux, float zc, int64_t T, int E, int K, int ld, float* dlogits, bf16* dl16, cudaStream_t st) {
     route_backward_kernel<<<static_cast<unsigned>((T + 7) / 8), 256, 0, st>>>(logits, idx, w, dw, counts, aux, zc, T, E, K, ld, dlogits, dl16);
+    return done();
+}
+
+int launch_router_dx(const bf16* dl, const bf16* Wr, int ld, const bf16* dx_perm, const int32_t* inv, int64_t T, int d, int K,
+                     void* dx, bool dx_bf16, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>((T + kDxTokens - 1) / kDxTokens), static_cast<unsigned>((d + kDxCols - 1) / kDxCols));
+    if (dx_bf16) router_dx_kernel<<<grid, 256, 0, st>>>(dl, Wr, ld, dx_perm, inv, T, d, K, static_cast<bf16*>(dx));
+    else router_dx_kernel<<<grid, 256, 0, st>>>(dl, Wr, ld, dx_perm, inv, T, d, K, static_cast<float*>(dx));
     return done();
 }
 

@@ -196,7 +196,7 @@ int moe_route_backward(const moe_dims* dims, const moe_bf16* x, const moe_bf16* 
             MOE_TRY(map_launch(launch_pad_router(w, d, E, L.ld, padded, st)));
             w = padded;
         }
-        MOE_TRY(map_launch(launch_train_router_dx(dl, T, L.ld, w, L.ld, E, d, in16(dx_perm), inv, K, dx, dx_is_bf16 != 0, status, st)));
+        MOE_TRY(map_launch(launch_router_dx(dl, w, L.ld, in16(dx_perm), inv, T, d, K, dx, dx_is_bf16 != 0, st)));
     }
     if (dWr) {
         float* part = reinterpret_cast<float*>(base + L.part);

@@ -11,7 +11,6 @@
 //   dw13    dW1 = X^T dG, dW3 = X^T dU                 (one launch)
 //   dw2     dW2 = H^T dY
 // and for the router, with dL [T, E] the logits' gradients:
-//   router dx   dx = sum of a token's rows + dL Wr^T   (gather in the epilogue)
 //   router dw   dWr = x^T dL                           (token chunks as groups)
 //
 // Every product is D[256 x 256] tiles of a CTA pair: CTA r holds the M half r
@@ -61,7 +60,7 @@ namespace moe {
 namespace {
 
 constexpr int kBK = 64;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr uint32_t kOperand = 16384u;  // one CTA's half of an operand: 128 x 64 bf16
 constexpr uint32_t kStageBytes = 2 * kOperand;
 constexpr uint32_t kTmemCols = 512;
@@ -70,7 +69,7 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxGroups = 256;
 constexpr int kRaster = 8;  // tile columns walked together: the operands of the ~74 tiles in flight stay in L2
 
-enum Epi : int { E_GATE, E_F32, E_DGATE, E_BF16, E_GATHER, E_WGRAD };
+enum Epi : int { E_GATE, E_F32, E_DGATE, E_BF16, E_WGRAD };
 
 struct Args {
     const int32_t* off;  // [G + 1] group offsets, or nullptr: groups of `chunk` rows
@@ -86,10 +85,7 @@ struct Args {
     void* out[2];
     bf16* h;               // E_GATE: activations out
     const bf16* gu;        // E_DGATE: saved projections [rows, 2 N]
-    int out_bf16;          // E_GATHER, E_WGRAD
-    const bf16* rows;      // E_GATHER: rows to add, or nullptr
-    const int32_t* inv;
-    int K;
+    int out_bf16;          // E_WGRAD: bf16 output, else fp32
     int* status;
     uint32_t wait_limit;
 };
@@ -214,13 +210,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// 8 consecutive values to 16 bytes of bf16 (round to nearest even).
-__device__ __forceinline__ void store8(bf16* dst, const float* v) {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+// 8 consecutive values as 16 bytes of bf16 (round to nearest even), and back.
+__device__ __forceinline__ uint4 pack8(const float* v) {
+    return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
-__device__ __forceinline__ void store8(float* dst, const float* v) {
-    reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void unpack8(const uint4& q, float* v) {
+    v[0] = bf_lo(q.x), v[1] = bf_hi(q.x), v[2] = bf_lo(q.y), v[3] = bf_hi(q.y);
+    v[4] = bf_lo(q.z), v[5] = bf_hi(q.z), v[6] = bf_lo(q.w), v[7] = bf_hi(q.w);
 }
 
 // Logistic function with the fast exponential and division: what comes of it
@@ -253,94 +249,174 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
     return __all_sync(0xffffffffu, wait_or_abort<CLUSTER>(bar, parity, a, code, abort_flag, peer_abort)) != 0;
 }
 
-// What the epilogue does with 32 accumulator columns (32-column chunk of the
-// tile at output column `col`) of output row `row`.
-template <int EPI>
-__device__ __forceinline__ void emit(const Args& a, const Tile& t, int64_t row, int col, const float* v, const float* u) {
-    if (EPI == E_GATE) {
-        bf16* gu = static_cast<bf16*>(a.out[0]) + row * a.ld;
-        bf16* h = a.h + row * a.N;
+// An accumulator has a row per lane; stored from there, one instruction would
+// touch 32 rows.  Each epilogue warp turns its 32 rows x 128 bytes round in 4 KB
+// of shared memory: 16-byte chunk j of row r sits at chunk j ^ (r mod 8), free
+// of bank conflicts by rows and by columns.  Then 8 lanes hold a row's 128
+// bytes: lane l has rows 4 i + l / 8, i < 8, and chunk l % 8 of each.
+__device__ __forceinline__ uint4* chunk_at(uint8_t* stg, int row, int j) {
+    return reinterpret_cast<uint4*>(stg + row * 128 + ((j ^ (row & 7)) << 4));
+}
+
+// The staged rows to global memory: `base` is row 0's first byte; rows and
+// 16-byte chunks beyond the counts are left out.
+__device__ __forceinline__ void flush(uint8_t* stg, int lane, uint8_t* base, int64_t row_bytes, int rows, int chunks) {
+    __syncwarp();
+    const int j = lane & 7;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            if (col + j >= a.N) break;
-            float hv[8];
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        if (r < rows && j < chunks) *reinterpret_cast<uint4*>(base + r * row_bytes + j * 16) = *chunk_at(stg, r, j);
+    }
+    __syncwarp();
+}
+
+// 64 accumulator columns turned round: acc[i] = 8 columns from 8 (l % 8) of row 4 i + l / 8.
+__device__ __forceinline__ void turn64(uint32_t taddr, uint8_t* stg, int lane, float (&acc)[8][8]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) hv[i] = v[j + i] * sigmoid(v[j + i]) * u[j + i];
-            store8(gu + col + j, v + j);
-            store8(gu + a.N + col + j, u + j);
-            store8(h + col + j, hv);
-        }
-    } else if (EPI == E_DGATE) {
-        bf16* dgu = static_cast<bf16*>(a.out[0]) + row * a.ld;
-        const bf16* gu = a.gu + row * a.ld;
+    for (int p = 0; p < 2; ++p) {
+        float w[32];
+        tmem_ld32(taddr + static_cast<uint32_t>(32 * p), w);
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            if (col + j >= a.N) break;
-            const uint4 gv = *reinterpret_cast<const uint4*>(gu + col + j);
-            const uint4 uv = *reinterpret_cast<const uint4*>(gu + a.N + col + j);
-            const uint32_t gs[4] = {gv.x, gv.y, gv.z, gv.w}, us[4] = {uv.x, uv.y, uv.z, uv.w};
-            float dg[8], du[8];
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(chunk_at(stg, lane, j)) = make_float4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        __syncwarp();
+        if (((lane >> 2) & 1) == p) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float g = (i & 1) ? bf_hi(gs[i >> 1]) : bf_lo(gs[i >> 1]);
-                const float uu = (i & 1) ? bf_hi(us[i >> 1]) : bf_lo(us[i >> 1]);
-                const float s = sigmoid(g);
-                dg[i] = v[j + i] * uu * s * (1.0f + g * (1.0f - s));
-                du[i] = v[j + i] * g * s;
+                const int r = 4 * i + (lane >> 3), j = 2 * (lane & 3);
+                const float4 a = *reinterpret_cast<const float4*>(chunk_at(stg, r, j));
+                const float4 b = *reinterpret_cast<const float4*>(chunk_at(stg, r, j + 1));
+                acc[i][0] = a.x, acc[i][1] = a.y, acc[i][2] = a.z, acc[i][3] = a.w;
+                acc[i][4] = b.x, acc[i][5] = b.y, acc[i][6] = b.z, acc[i][7] = b.w;
             }
-            store8(dgu + col + j, dg);
-            store8(dgu + a.N + col + j, du);
         }
-    } else if (EPI == E_F32) {
-        float* out = static_cast<float*>(a.out[0]) + row * a.ld;
-#pragma unroll
-        for (int j = 0; j < 32; j += 8)
-            if (col + j < a.N) store8(out + col + j, v + j);
-    } else if (EPI == E_BF16) {
-        bf16* out = static_cast<bf16*>(a.out[0]) + row * a.ld;
-#pragma unroll
-        for (int j = 0; j < 32; j += 8)
-            if (col + j < a.N) store8(out + col + j, v + j);
-    } else if (EPI == E_GATHER) {
-        float s[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = v[i];
-        if (a.rows != nullptr)
-            for (int k = 0; k < a.K; ++k) {
-                const int r = a.inv[row * a.K + k];
-                if (static_cast<unsigned>(r) >= static_cast<unsigned>(a.cap * a.K)) continue;  // dropped
-                const bf16* src = a.rows + static_cast<int64_t>(r) * a.ld;
-#pragma unroll
-                for (int j = 0; j < 32; j += 8) {
-                    if (col + j >= a.N) break;
-                    const uint4 q = *reinterpret_cast<const uint4*>(src + col + j);
-                    s[j + 0] += bf_lo(q.x);
-                    s[j + 1] += bf_hi(q.x);
-                    s[j + 2] += bf_lo(q.y);
-                    s[j + 3] += bf_hi(q.y);
-                    s[j + 4] += bf_lo(q.z);
-                    s[j + 5] += bf_hi(q.z);
-                    s[j + 6] += bf_lo(q.w);
-                    s[j + 7] += bf_hi(q.w);
-                }
-            }
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            if (col + j >= a.N) break;
-            if (a.out_bf16) store8(static_cast<bf16*>(a.out[0]) + row * a.ld + col + j, s + j);
-            else store8(static_cast<float*>(a.out[0]) + row * a.ld + col + j, s + j);
-        }
-    } else {  // E_WGRAD
-        const int sel = t.n >= a.n_first ? 1 : 0;
-        const int64_t at = (static_cast<int64_t>(t.g) * a.M + row) * a.ld;
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            if (col + j >= a.N) break;
-            if (a.out_bf16) store8(static_cast<bf16*>(a.out[sel]) + at + col + j, v + j);
-            else store8(static_cast<float*>(a.out[sel]) + at + col + j, v + j);
-        }
+        __syncwarp();
     }
 }
+
+// 64 accumulator columns rounded to bf16, staged a row per lane.
+__device__ __forceinline__ void stage64(uint32_t taddr, uint8_t* stg, int lane) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        float v[32];
+        tmem_ld32(taddr + static_cast<uint32_t>(32 * p), v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *chunk_at(stg, lane, 4 * p + j) = pack8(v + 8 * j);
+    }
+}
+
+// A warp's part of a tile: 32 rows (`rows` of them valid) from output row
+// `row0`, columns from `col0` up to the width N: 128 of them, 64 of each
+// projection for E_GATE.  `taddr` is its first accumulator column.
+// E_DGATE reads the saved projections at the same places; `load` (before the
+// accumulator is ready) fetches the first 64 columns' worth.
+template <int EPI>
+struct Epilogue {
+    const Args& a;
+    uint8_t* stg;
+    int lane;
+    uint4 g[EPI == E_DGATE ? 8 : 1], u[EPI == E_DGATE ? 8 : 1];
+
+    __device__ __forceinline__ int chunks(int col, int per) const { return (a.N - col) / per; }  // N is a multiple of 8
+
+    // Every load is issued, at a place clamped into the tensor where its row or
+    // column is out: a branch around each would wait for them in turn.
+    __device__ __forceinline__ void load(int64_t row0, int rows, int col) {
+        const int c = min(col + 8 * (lane & 7), a.N - 8);
+        if constexpr (EPI == E_DGATE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = min(4 * i + (lane >> 3), rows - 1);
+                const bf16* p = a.gu + (row0 + r) * a.ld + c;
+                g[i] = __ldcs(reinterpret_cast<const uint4*>(p));
+                u[i] = __ldcs(reinterpret_cast<const uint4*>(p + a.N));
+            }
+        }
+    }
+
+    __device__ __forceinline__ void run(uint32_t taddr, int64_t row0, int rows, int col0, int sel) {
+        if (EPI == E_GATE) {
+            if (col0 >= a.N) return;
+            const int n = chunks(col0, 8);
+            uint8_t* gu = reinterpret_cast<uint8_t*>(static_cast<bf16*>(a.out[0]) + row0 * a.ld + col0);
+            stage64(taddr, stg, lane);
+            flush(stg, lane, gu, a.ld * 2, rows, n);
+            stage64(taddr + 128, stg, lane);
+            flush(stg, lane, gu + static_cast<int64_t>(a.N) * 2, a.ld * 2, rows, n);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float v[32], w[32];
+                tmem_ld32(taddr + static_cast<uint32_t>(32 * p), v);
+                tmem_ld32(taddr + static_cast<uint32_t>(128 + 32 * p), w);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= sigmoid(v[i]) * w[i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *chunk_at(stg, lane, 4 * p + j) = pack8(v + 8 * j);
+            }
+            flush(stg, lane, reinterpret_cast<uint8_t*>(a.h + row0 * a.N + col0), static_cast<int64_t>(a.N) * 2, rows, n);
+        } else if constexpr (EPI == E_DGATE) {
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int col = col0 + 64 * half;
+                if (col >= a.N) return;
+                if (half) load(row0, rows, col);
+                const int c = col + 8 * (lane & 7);
+                float acc[8][8];
+                turn64(taddr + static_cast<uint32_t>(64 * half), stg, lane, acc);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3);
+                    float gv[8], uv[8], dg[8], du[8];
+                    unpack8(g[i], gv);
+                    unpack8(u[i], uv);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const float sg = sigmoid(gv[x]);
+                        dg[x] = acc[i][x] * uv[x] * sg * (1.0f + gv[x] * (1.0f - sg));
+                        du[x] = acc[i][x] * gv[x] * sg;
+                    }
+                    if (r < rows && c < a.N) {
+                        bf16* dst = static_cast<bf16*>(a.out[0]) + (row0 + r) * a.ld + c;
+                        *reinterpret_cast<uint4*>(dst) = pack8(dg);
+                        *reinterpret_cast<uint4*>(dst + a.N) = pack8(du);
+                    }
+                }
+            }
+        } else if (EPI == E_BF16 || (EPI == E_WGRAD && a.out_bf16)) {
+            bf16* out = static_cast<bf16*>(a.out[sel]) + row0 * a.ld;
+            for (int half = 0; half < 2; ++half) {
+                const int col = col0 + 64 * half;
+                if (col >= a.N) return;
+                stage64(taddr + static_cast<uint32_t>(64 * half), stg, lane);
+                flush(stg, lane, reinterpret_cast<uint8_t*>(out + col), a.ld * 2, rows, chunks(col, 8));
+            }
+        } else {
+            float* out = static_cast<float*>(a.out[sel]) + row0 * a.ld;
+            for (int c = 0; c < 4; ++c) {
+                const int col = col0 + 32 * c;
+                if (col >= a.N) return;
+                float v[32];
+                tmem_ld32(taddr + static_cast<uint32_t>(32 * c), v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<float4*>(chunk_at(stg, lane, j)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                flush(stg, lane, reinterpret_cast<uint8_t*>(out + col), a.ld * 4, rows, chunks(col, 4));
+            }
+        }
+    }
+
+    // A weight gradient of an expert without rows.
+    __device__ __forceinline__ void zero(int64_t row0, int rows, int col0, int sel) {
+        const int per = a.out_bf16 ? 8 : 4;
+        for (int r = 0; r < rows; ++r)
+            for (int c = col0 + per * lane; c < a.N && c < col0 + 128; c += 32 * per) {
+                const int64_t at = (row0 + r) * a.ld + c;
+                uint8_t* p = static_cast<uint8_t*>(a.out[sel]) + at * (a.out_bf16 ? 2 : 4);
+                *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
+            }
+    }
+};
 
 template <int EPI, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -348,7 +424,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     constexpr bool WG = EPI == E_WGRAD;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes + kEpiWarps * 4096);
     uint64_t* empty = full + kStages;
     uint64_t* tail = empty + kStages;
     uint64_t* clear = tail + kStages;
@@ -558,42 +634,28 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         // a quarter take the two column halves.
         const int q = warp & 3, half = (warp - 2) >> 2;
         const uint32_t leader_tempty = peer_addr(smem_u32(tempty), 0);
+        Epilogue<EPI> epi{a, smem + kStages * kStageBytes + (warp - 2) * 4096, lane};
         int it = 0;
         for (int tile = pair; tile < sc.total; tile += npairs) {
             const Tile t = decode<WG>(a, sc, tile);
-            const int r = static_cast<int>(rank) * 128 + q * 32 + lane;  // row of the tile
-            const bool valid = WG ? t.m * 256 + r < a.M : r < t.rows;
-            const int64_t row = WG ? t.m * 256 + r : t.row0 + r;
+            const int r0 = static_cast<int>(rank) * 128 + q * 32;  // this warp's first row of the tile
+            const int rows = max(0, min(32, (WG ? a.M - t.m * 256 : t.rows) - r0));
+            const int64_t row0 = WG ? static_cast<int64_t>(t.g) * a.M + t.m * 256 + r0 : t.row0 + r0;
             const int sel = WG && t.n >= a.n_first ? 1 : 0;
             const int col0 = (t.n - sel * a.n_first) * (EPI == E_GATE ? 128 : 256) + half * (EPI == E_GATE ? 64 : 128);
-            float v[32], u[32];
-            if (WG && t.kb == 0) {  // no rows: the gradient is zero
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                for (int c = 0; c < 4; ++c)
-                    if (valid) emit<EPI>(a, t, row, col0 + 32 * c, v, u);
+            if (WG && t.kb == 0) {
+                epi.zero(row0, rows, col0, sel);
                 continue;
             }
             const int buf = it & 1;
             const uint32_t use = static_cast<uint32_t>(it >> 1);
             ++it;
+            if (rows > 0 && col0 < a.N) epi.load(row0, rows, col0);
             if (!warp_wait(&tfull[buf], use & 1u, a, DEV_TIMEOUT_EPI_TFULL, abort_flag, peer_abort)) break;
             tc_fence_after();
-            const uint32_t taddr = tmem_base + static_cast<uint32_t>(buf) * 256u + (static_cast<uint32_t>(q * 32) << 16);
-            if (EPI == E_GATE) {
-                for (int c = 0; c < 2; ++c) {
-                    tmem_ld32(taddr + static_cast<uint32_t>(half * 64 + c * 32), v);
-                    tmem_ld32(taddr + static_cast<uint32_t>(128 + half * 64 + c * 32), u);
-                    if (valid) emit<EPI>(a, t, row, col0 + 32 * c, v, u);
-                    __syncwarp();
-                }
-            } else {
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32(taddr + static_cast<uint32_t>(half * 128 + c * 32), v);
-                    if (valid) emit<EPI>(a, t, row, col0 + 32 * c, v, u);
-                    __syncwarp();
-                }
-            }
+            const uint32_t taddr = tmem_base + static_cast<uint32_t>(buf) * 256u + (static_cast<uint32_t>(q * 32) << 16) +
+                                   static_cast<uint32_t>(half * (EPI == E_GATE ? 64 : 128));
+            if (rows > 0) epi.run(taddr, row0, rows, col0, sel);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(leader_tempty + 8u * buf);
@@ -664,7 +726,7 @@ bool map_weights(CUtensorMap* m, const bf16* base, int64_t mats, int64_t rows, i
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-constexpr size_t kSmem = 1024 + kStages * kStageBytes + (4 * kStages + 5) * 8 + 24 + 2 * (kMaxGroups + 1) * 4;
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * 4096 + (4 * kStages + 5) * 8 + 24 + 2 * (kMaxGroups + 1) * 4;
 
 template <int EPI, bool B_MN>
 int launch(const Maps& maps, Args a, int max_pairs, cudaStream_t st) {
@@ -801,31 +863,6 @@ int launch_train_dw(const bf16* left, int m_cols, const bf16* right0, const bf16
     a.status = status;
     const int64_t tiles = static_cast<int64_t>(G) * a.m_tiles * a.n_tiles;
     return launch<E_WGRAD, true>(m, a, tiles > (1 << 20) ? (1 << 20) : static_cast<int>(tiles), st);
-}
-
-int launch_train_router_dx(const bf16* dl, int64_t T, int dl_ld, const bf16* Wr, int wr_ld, int E, int d, const bf16* rows,
-                           const int32_t* inv, int K, void* dx, bool dx_bf16, int* status, cudaStream_t st) {
-    Maps m;
-    std::memset(&m, 0, sizeof(m));
-    if (!map_matrix(&m.a[0], dl, T, E, dl_ld, 128) || !map_weights(&m.b[0], Wr, 1, d, wr_ld, 128)) return -3;
-    m.a[1] = m.a[0];
-    m.b[1] = m.b[0];
-    Args a{};
-    a.off = nullptr;
-    a.chunk = T;
-    a.cap = T;
-    a.G = 1;
-    a.N = d;
-    a.n_tiles = ceil_div(d, 256);
-    a.kb_first = a.kb_all = ceil_div(E, kBK);
-    a.ld = d;
-    a.out[0] = dx;
-    a.out_bf16 = dx_bf16 ? 1 : 0;
-    a.rows = rows;
-    a.inv = inv;
-    a.K = K;
-    a.status = status;
-    return launch<E_GATHER, false>(m, a, tile_bound(T, 1, a.n_tiles), st);
 }
 
 }  // namespace moe
