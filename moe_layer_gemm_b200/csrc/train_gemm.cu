@@ -60,14 +60,15 @@ namespace moe {
 namespace {
 
 constexpr int kBK = 64;
-constexpr int kStages = 5;
 constexpr uint32_t kOperand = 16384u;  // one CTA's half of an operand: 128 x 64 bf16
-constexpr uint32_t kStageBytes = 2 * kOperand;
+constexpr uint32_t kRingBytes = 12 * kOperand;
+constexpr int kStaging = 2048;  // per epilogue warp
 constexpr uint32_t kTmemCols = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxGroups = 256;
-constexpr int kRaster = 8;  // tile columns walked together: the operands of the ~74 tiles in flight stay in L2
+constexpr int kMaxStages = 6;
+constexpr int kRaster = 3;  // tile columns walked together: the operands of the ~74 tiles in flight stay in L2
 
 enum Epi : int { E_GATE, E_F32, E_DGATE, E_BF16, E_WGRAD };
 
@@ -78,7 +79,7 @@ struct Args {
     int G;
     int M;             // weight gradients: output rows of a group
     int N;             // output columns (E_GATE: of each projection)
-    int n_tiles, m_tiles;
+    int n_tiles, m_tiles;  // column tiles (of SUB sub-tiles), row tiles of a weight gradient
     int kb_first, kb_all;  // k-blocks of the first operand pair, and of both (token-major products)
     int n_first;           // weight gradients: column tiles of the first output
     int64_t ld;            // output row stride
@@ -250,84 +251,60 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 }
 
 // An accumulator has a row per lane; stored from there, one instruction would
-// touch 32 rows.  Each epilogue warp turns its 32 rows x 128 bytes round in 4 KB
-// of shared memory: 16-byte chunk j of row r sits at chunk j ^ (r mod 8), free
-// of bank conflicts by rows and by columns.  Then 8 lanes hold a row's 128
-// bytes: lane l has rows 4 i + l / 8, i < 8, and chunk l % 8 of each.
+// touch 32 rows.  Each epilogue warp turns 32 rows x 64 bytes at a time round in
+// 2 KB of shared memory: 16-byte chunk j of row r sits at chunk
+// j ^ (r / 2 mod 4), free of bank conflicts by rows and by columns.  Then 4
+// lanes hold a row's 64 bytes: lane l has rows 8 i + l / 4, i < 4, and chunk
+// l % 4 of each.
 __device__ __forceinline__ uint4* chunk_at(uint8_t* stg, int row, int j) {
-    return reinterpret_cast<uint4*>(stg + row * 128 + ((j ^ (row & 7)) << 4));
+    return reinterpret_cast<uint4*>(stg + row * 64 + ((j ^ ((row >> 1) & 3)) << 4));
 }
 
 // The staged rows to global memory: `base` is row 0's first byte; rows and
 // 16-byte chunks beyond the counts are left out.
 __device__ __forceinline__ void flush(uint8_t* stg, int lane, uint8_t* base, int64_t row_bytes, int rows, int chunks) {
     __syncwarp();
-    const int j = lane & 7;
+    const int j = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
         if (r < rows && j < chunks) *reinterpret_cast<uint4*>(base + r * row_bytes + j * 16) = *chunk_at(stg, r, j);
     }
     __syncwarp();
 }
 
-// 64 accumulator columns turned round: acc[i] = 8 columns from 8 (l % 8) of row 4 i + l / 8.
-__device__ __forceinline__ void turn64(uint32_t taddr, uint8_t* stg, int lane, float (&acc)[8][8]) {
+// A row's 32 values, rounded to bf16.
+__device__ __forceinline__ void stage_bf16(uint8_t* stg, int lane, const float* v) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        float w[32];
-        tmem_ld32(taddr + static_cast<uint32_t>(32 * p), w);
+    for (int j = 0; j < 4; ++j) *chunk_at(stg, lane, j) = pack8(v + 8 * j);
+}
+// 16 of them as they are.
+__device__ __forceinline__ void stage_f32(uint8_t* stg, int lane, const float* v) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float4*>(chunk_at(stg, lane, j)) = make_float4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        __syncwarp();
-        if (((lane >> 2) & 1) == p) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 4 * i + (lane >> 3), j = 2 * (lane & 3);
-                const float4 a = *reinterpret_cast<const float4*>(chunk_at(stg, r, j));
-                const float4 b = *reinterpret_cast<const float4*>(chunk_at(stg, r, j + 1));
-                acc[i][0] = a.x, acc[i][1] = a.y, acc[i][2] = a.z, acc[i][3] = a.w;
-                acc[i][4] = b.x, acc[i][5] = b.y, acc[i][6] = b.z, acc[i][7] = b.w;
-            }
-        }
-        __syncwarp();
-    }
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(chunk_at(stg, lane, j)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
-// 64 accumulator columns rounded to bf16, staged a row per lane.
-__device__ __forceinline__ void stage64(uint32_t taddr, uint8_t* stg, int lane) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        float v[32];
-        tmem_ld32(taddr + static_cast<uint32_t>(32 * p), v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) *chunk_at(stg, lane, 4 * p + j) = pack8(v + 8 * j);
-    }
-}
-
-// A warp's part of a tile: 32 rows (`rows` of them valid) from output row
-// `row0`, columns from `col0` up to the width N: 128 of them, 64 of each
-// projection for E_GATE.  `taddr` is its first accumulator column.
+// A warp's part of a 256-column sub-tile: 32 rows (`rows` of them valid) from
+// output row `row0`, columns from `col0` up to the width N: 128 of them, 64 of
+// each projection for E_GATE.  `taddr` is its first accumulator column.
 // E_DGATE reads the saved projections at the same places; `load` (before the
-// accumulator is ready) fetches the first 64 columns' worth.
+// accumulator is ready) fetches the first 32 columns' worth.
 template <int EPI>
 struct Epilogue {
     const Args& a;
     uint8_t* stg;
     int lane;
-    uint4 g[EPI == E_DGATE ? 8 : 1], u[EPI == E_DGATE ? 8 : 1];
-
-    __device__ __forceinline__ int chunks(int col, int per) const { return (a.N - col) / per; }  // N is a multiple of 8
+    uint4 g[EPI == E_DGATE ? 4 : 1], u[EPI == E_DGATE ? 4 : 1];
 
     // Every load is issued, at a place clamped into the tensor where its row or
     // column is out: a branch around each would wait for them in turn.
     __device__ __forceinline__ void load(int64_t row0, int rows, int col) {
-        const int c = min(col + 8 * (lane & 7), a.N - 8);
         if constexpr (EPI == E_DGATE) {
+            const int c = min(col + 8 * (lane & 3), a.N - 8);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = min(4 * i + (lane >> 3), rows - 1);
+            for (int i = 0; i < 4; ++i) {
+                const int r = min(8 * i + (lane >> 2), rows - 1);
                 const bf16* p = a.gu + (row0 + r) * a.ld + c;
                 g[i] = __ldcs(reinterpret_cast<const uint4*>(p));
                 u[i] = __ldcs(reinterpret_cast<const uint4*>(p + a.N));
@@ -336,40 +313,60 @@ struct Epilogue {
     }
 
     __device__ __forceinline__ void run(uint32_t taddr, int64_t row0, int rows, int col0, int sel) {
-        if (EPI == E_GATE) {
-            if (col0 >= a.N) return;
-            const int n = chunks(col0, 8);
-            uint8_t* gu = reinterpret_cast<uint8_t*>(static_cast<bf16*>(a.out[0]) + row0 * a.ld + col0);
-            stage64(taddr, stg, lane);
-            flush(stg, lane, gu, a.ld * 2, rows, n);
-            stage64(taddr + 128, stg, lane);
-            flush(stg, lane, gu + static_cast<int64_t>(a.N) * 2, a.ld * 2, rows, n);
-#pragma unroll
+        if constexpr (EPI == E_GATE) {
+#pragma unroll 1
             for (int p = 0; p < 2; ++p) {
+                const int col = col0 + 32 * p, n = (a.N - col) / 8;
+                if (col >= a.N) return;
                 float v[32], w[32];
                 tmem_ld32(taddr + static_cast<uint32_t>(32 * p), v);
                 tmem_ld32(taddr + static_cast<uint32_t>(128 + 32 * p), w);
+                uint8_t* gu = reinterpret_cast<uint8_t*>(static_cast<bf16*>(a.out[0]) + row0 * a.ld + col);
+                stage_bf16(stg, lane, v);
+                flush(stg, lane, gu, a.ld * 2, rows, n);
+                stage_bf16(stg, lane, w);
+                flush(stg, lane, gu + static_cast<int64_t>(a.N) * 2, a.ld * 2, rows, n);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= sigmoid(v[i]) * w[i];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) *chunk_at(stg, lane, 4 * p + j) = pack8(v + 8 * j);
+                stage_bf16(stg, lane, v);
+                flush(stg, lane, reinterpret_cast<uint8_t*>(a.h + row0 * a.N + col), static_cast<int64_t>(a.N) * 2, rows, n);
             }
-            flush(stg, lane, reinterpret_cast<uint8_t*>(a.h + row0 * a.N + col0), static_cast<int64_t>(a.N) * 2, rows, n);
         } else if constexpr (EPI == E_DGATE) {
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                const int col = col0 + 64 * half;
+            for (int p = 0; p < 4; ++p) {
+                const int col = col0 + 32 * p, c = col + 8 * (lane & 3);
                 if (col >= a.N) return;
-                if (half) load(row0, rows, col);
-                const int c = col + 8 * (lane & 7);
-                float acc[8][8];
-                turn64(taddr + static_cast<uint32_t>(64 * half), stg, lane, acc);
+                float acc[4][8];
+                {
+                    float v[32];
+                    tmem_ld32(taddr + static_cast<uint32_t>(32 * p), v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 4 * i + (lane >> 3);
+                    for (int h = 0; h < 2; ++h) {  // 16 columns at a time; lanes l % 4 = 2 h, 2 h + 1 take them
+                        stage_f32(stg, lane, v + 16 * h);
+                        __syncwarp();
+                        if (((lane >> 1) & 1) == h) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = 8 * i + (lane >> 2), j = 2 * (lane & 1);
+                                const float4 x = *reinterpret_cast<const float4*>(chunk_at(stg, r, j));
+                                const float4 y = *reinterpret_cast<const float4*>(chunk_at(stg, r, j + 1));
+                                acc[i][0] = x.x, acc[i][1] = x.y, acc[i][2] = x.z, acc[i][3] = x.w;
+                                acc[i][4] = y.x, acc[i][5] = y.y, acc[i][6] = y.z, acc[i][7] = y.w;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+                uint4 gn[4], un[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gn[i] = g[i], un[i] = u[i];
+                if (p < 3 && col + 32 < a.N) load(row0, rows, col + 32);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + (lane >> 2);
                     float gv[8], uv[8], dg[8], du[8];
-                    unpack8(g[i], gv);
-                    unpack8(u[i], uv);
+                    unpack8(gn[i], gv);
+                    unpack8(un[i], uv);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         const float sg = sigmoid(gv[x]);
@@ -383,25 +380,25 @@ struct Epilogue {
                     }
                 }
             }
-        } else if (EPI == E_BF16 || (EPI == E_WGRAD && a.out_bf16)) {
-            bf16* out = static_cast<bf16*>(a.out[sel]) + row0 * a.ld;
-            for (int half = 0; half < 2; ++half) {
-                const int col = col0 + 64 * half;
-                if (col >= a.N) return;
-                stage64(taddr + static_cast<uint32_t>(64 * half), stg, lane);
-                flush(stg, lane, reinterpret_cast<uint8_t*>(out + col), a.ld * 2, rows, chunks(col, 8));
-            }
         } else {
-            float* out = static_cast<float*>(a.out[sel]) + row0 * a.ld;
-            for (int c = 0; c < 4; ++c) {
-                const int col = col0 + 32 * c;
+            const bool as_bf16 = EPI == E_BF16 || (EPI == E_WGRAD && a.out_bf16);
+            const int bytes = as_bf16 ? 2 : 4;
+            uint8_t* out = static_cast<uint8_t*>(a.out[sel]) + row0 * a.ld * bytes;
+#pragma unroll 1
+            for (int p = 0; p < 4; ++p) {
+                const int col = col0 + 32 * p;
                 if (col >= a.N) return;
                 float v[32];
-                tmem_ld32(taddr + static_cast<uint32_t>(32 * c), v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float4*>(chunk_at(stg, lane, j)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                flush(stg, lane, reinterpret_cast<uint8_t*>(out + col), a.ld * 4, rows, chunks(col, 4));
+                tmem_ld32(taddr + static_cast<uint32_t>(32 * p), v);
+                if (as_bf16) {
+                    stage_bf16(stg, lane, v);
+                    flush(stg, lane, out + col * 2, a.ld * 2, rows, (a.N - col) / 8);
+                } else {
+                    stage_f32(stg, lane, v);
+                    flush(stg, lane, out + static_cast<int64_t>(col) * 4, a.ld * 4, rows, (a.N - col) / 4);
+                    stage_f32(stg, lane, v + 16);
+                    flush(stg, lane, out + static_cast<int64_t>(col) * 4 + 64, a.ld * 4, rows, (a.N - col) / 4 - 4);
+                }
             }
         }
     }
@@ -418,13 +415,23 @@ struct Epilogue {
     }
 };
 
-template <int EPI, bool B_MN>
+// SUB: 256-column sub-tiles of a tile, each with an accumulator of its own.  With
+// one, the two accumulators alternate and a tile's epilogue runs under the
+// next tile's MMAs.  With two, both belong to the tile: a k-block of A serves
+// twice the MMAs, so a ring of the same size reaches twice as far ahead and
+// 3/4 of the bytes are loaded; in exchange the next tile waits for the
+// epilogue, except that up to a ring of its k-blocks are multiplied into the
+// first accumulator while the second is still being read.
+template <int EPI, bool B_MN, int SUB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     constexpr bool WG = EPI == E_WGRAD;
+    constexpr uint32_t kStageBytes = (1 + SUB) * kOperand;
+    constexpr int kStages = kRingBytes / kStageBytes;
+    constexpr int kSubCols = EPI == E_GATE ? 128 : 256;  // output columns of a sub-tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes + kEpiWarps * 4096);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes + kEpiWarps * kStaging);
     uint64_t* empty = full + kStages;
     uint64_t* tail = empty + kStages;
     uint64_t* clear = tail + kStages;
@@ -433,8 +440,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    uint32_t* issued = tmem_slot + 2;  // [rank][stage uses issued, which stages' last use was a tail]
-    int* off = reinterpret_cast<int*>(tmem_slot + 6);
+    uint32_t* issued = tmem_slot + 2;  // [rank][stage uses issued, stages whose last use was a tail], [rank][use_bytes]
+    int* off = reinterpret_cast<int*>(issued + 4 + 2 * kMaxStages);
     int* start = off + kMaxGroups + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -501,46 +508,57 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             // ------------------------------------------------ producer (both CTAs)
             const uint32_t leader_full = peer_addr(smem_u32(full), 0), own_tail = peer_addr(smem_u32(tail), rank);
             uint32_t s = 0, ph = 0, uses = 0, tails = 0, tail_ph = 0;
+            uint32_t* use_bytes = issued + 4 + kMaxStages * rank;  // this CTA's bytes of each stage's last use
             bool ok = true;
             for (int tile = pair; ok && tile < sc.total; tile += npairs) {
                 const Tile t = decode<WG>(a, sc, tile);
                 const int sel = WG && t.n >= a.n_first ? 1 : 0;
-                const int n0 = WG ? (t.n - sel * a.n_first) * 256 + 128 * static_cast<int>(rank)
-                                  : (EPI == E_GATE ? t.n * 128 : t.n * 256 + 128 * static_cast<int>(rank));
+                const int col0 = (t.n - sel * a.n_first) * SUB * kSubCols;
+                const int subs = min(SUB, (a.N - col0 + kSubCols - 1) / kSubCols);
+                const int n0 = col0 + (EPI == E_GATE ? 0 : 128 * static_cast<int>(rank));
+                const uint32_t bytes = static_cast<uint32_t>(1 + subs) * kOperand;
                 for (int kb = 0; kb < t.kb; ++kb) {
                     if (!wait_or_abort(&empty[s], ph ^ 1u, a, DEV_TIMEOUT_PRODUCER_EMPTY, abort_flag, peer_abort)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t sa = smem_u32(smem + s * kStageBytes), sb = sa + kOperand;
+                    const uint32_t sa = smem_u32(smem + s * kStageBytes);
                     uint32_t bar = leader_full + 8u * s;
                     if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
                         bar = own_tail + 8u * s;
-                        mbar_arrive_expect_tx(&tail[s], kStageBytes);
+                        mbar_arrive_expect_tx(&tail[s], bytes);
                         if (leader) mbar_arrive(&full[s]);
                         tails |= 1u << s;
                         tail_ph ^= 1u << s;
                     } else {
-                        if (leader) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                        if (leader) mbar_arrive_expect_tx(&full[s], 2 * bytes);
                         tails &= ~(1u << s);
                     }
+                    use_bytes[s] = bytes;
                     if (WG) {
                         const int y = static_cast<int>(t.row0) + kb * kBK;
                         const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
                         load_2d(&maps.a[0], sa, bar, m0, y);
                         load_2d(&maps.a[0], sa + 8192, bar, m0 + 64, y);
-                        load_2d(&maps.b[sel], sb, bar, n0, y);
-                        load_2d(&maps.b[sel], sb + 8192, bar, n0 + 64, y);
+                        for (int j = 0; j < subs; ++j) {
+                            const uint32_t sb = sa + (1 + j) * kOperand;
+                            load_2d(&maps.b[sel], sb, bar, n0 + 256 * j, y);
+                            load_2d(&maps.b[sel], sb + 8192, bar, n0 + 256 * j + 64, y);
+                        }
                     } else {
                         const int second = kb >= a.kb_first ? 1 : 0;
                         const int k0 = (kb - (second ? a.kb_first : 0)) * kBK;
                         load_2d(&maps.a[second], sa, bar, k0, static_cast<int>(t.row0) + 128 * static_cast<int>(rank));
                         const CUtensorMap* b = EPI == E_GATE ? &maps.b[rank] : &maps.b[second];
-                        if (B_MN) {
-                            load_3d(b, sb, bar, n0, k0, t.g);
-                            load_3d(b, sb + 8192, bar, n0 + 64, k0, t.g);
-                        } else {
-                            load_3d(b, sb, bar, k0, n0, t.g);
+                        for (int j = 0; j < subs; ++j) {
+                            const uint32_t sb = sa + (1 + j) * kOperand;
+                            const int n = n0 + kSubCols * j;
+                            if (B_MN) {
+                                load_3d(b, sb, bar, n, k0, t.g);
+                                load_3d(b, sb + 8192, bar, n + 64, k0, t.g);
+                            } else {
+                                load_3d(b, sb, bar, k0, n, t.g);
+                            }
                         }
                     }
                     ++uses;
@@ -550,77 +568,119 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             // this CTA's own tails have landed (a phase never used counts as complete)
             for (int i = 0; WG && i < kStages; ++i)
                 mbar_drain(&tail[i], ((tail_ph >> i) & 1u) ^ 1u, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
-            const uint32_t rec = peer_addr(smem_u32(issued + 2 * rank), 0);
-            store_cluster(rec, uses);
-            store_cluster(rec + 4, tails);
+            const uint32_t rec = peer_addr(smem_u32(issued), 0);
+            store_cluster(rec + 8u * rank, uses);
+            store_cluster(rec + 8u * rank + 4u, tails);
+            if (!leader)
+                for (int i = 0; i < kStages; ++i) store_cluster(rec + 4u * (4 + kMaxStages + i), use_bytes[i]);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer (leader); the peer only clears tails
         // idesc: D fp32, A and B bf16, bits 15 and 16 set where A, B are M-, N-contiguous
         constexpr uint32_t idesc = umma_idesc_bf16(256, 256) | (WG ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
         const uint32_t leader_clear = peer_addr(smem_u32(clear), 0);
-        uint32_t s = 0, ph = 0, tail_ph = 0;
+        uint32_t s = 0, ph = 0, tail_ph = 0, uses1 = 0;  // uses1: tiles that filled the second of two sub-tiles
         int it = 0;
         bool ok = true;
+        // Wait until k-block kb of the tile is in stage s of both CTAs, a
+        // tail's rows behind the group cleared; the 16-k steps to multiply, 0: abort.
+        auto arrived = [&](const Tile& t, int kb, int subs) -> int {
+            int steps = kBK / 16;
+            if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
+                const uint32_t tph = (tail_ph >> s) & 1u;
+                tail_ph ^= 1u << s;
+                if (!warp_wait(&tail[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
+                steps = (t.k_tail + 15) / 16;
+                const int from = t.k_tail * 8, to = steps * 16 * 8;  // 16-byte units of a 64-column box
+                uint4* box = reinterpret_cast<uint4*>(smem + s * kStageBytes);
+                for (int i = from + lane; i < to; i += 32)
+                    for (int b = 0; b < 2 + 2 * subs; ++b) box[b * 512 + i] = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (!leader) {
+                    if (lane == 0) arrive_cluster(leader_clear + 8u * s);
+                } else if (!warp_wait<true>(&clear[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
+                    return 0;
+                }
+            }
+            if (leader && !warp_wait(&full[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
+            tc_fence_after();
+            return steps;
+        };
+        // Stage `st`'s k-block into accumulator `buf` with sub-tile j of B.
+        auto multiply = [&](uint32_t st, int j, int buf, int steps, bool first) {
+            const uint32_t stage = smem_u32(smem + st * kStageBytes), d_tmem = tmem_base + static_cast<uint32_t>(buf) * 256u;
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk) {
+                if (WG && kk >= steps) break;
+                const uint32_t sb = stage + (1 + j) * kOperand;
+                const uint64_t da = WG ? desc_mn(stage + kk * 2048) : umma_desc_sw128(stage + kk * 32);
+                const uint64_t db = B_MN ? desc_mn(sb + kk * 2048) : umma_desc_sw128(sb + kk * 32);
+                mma_pair(d_tmem, da, db, idesc, (!first || kk > 0) ? 1u : 0u);
+            }
+        };
         for (int tile = pair; ok && (WG || leader) && tile < sc.total; tile += npairs) {
             const Tile t = decode<WG>(a, sc, tile);
             if (t.kb == 0) continue;
-            const int buf = it & 1;
-            const uint32_t use = static_cast<uint32_t>(it >> 1);
-            ++it;
+            const int col0 = (t.n - (WG && t.n >= a.n_first ? a.n_first : 0)) * SUB * kSubCols;
+            const int subs = SUB == 1 ? 1 : min(SUB, (a.N - col0 + kSubCols - 1) / kSubCols);
+            int kb = 0;
             if (leader) {
+                const int buf = SUB == 1 ? it & 1 : 0;
+                const uint32_t use = static_cast<uint32_t>(SUB == 1 ? it >> 1 : it);
                 if (!warp_wait<true>(&tempty[buf], (use & 1u) ^ 1u, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
                 tc_fence_after();
-            }
-            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf) * 256u;
-            for (int kb = 0; kb < t.kb; ++kb) {
-                const uint32_t stage = smem_u32(smem + s * kStageBytes);
-                int steps = kBK / 16;
-                if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
-                    // the group ends inside this box: clear the rows behind it up
-                    // to the last 16-row step that is multiplied
-                    const uint32_t tph = (tail_ph >> s) & 1u;
-                    tail_ph ^= 1u << s;
-                    if (!warp_wait(&tail[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
-                        ok = false;
-                        break;
+                if (SUB == 2 && subs == 2) {
+                    // the second accumulator may still be read: go ahead in the first
+                    // with the k-blocks that the ring holds (whole ones, before any tail)
+                    const uint32_t s0 = s, ph0 = ph;
+                    const uint32_t want = (uses1 & 1u) ^ 1u;
+                    while (kb < kStages && kb < t.kb - 1) {
+                        if (__all_sync(0xffffffffu, try_wait_cluster(&tempty[1], want))) break;
+                        if (!arrived(t, kb, subs)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) multiply(s, 0, 0, kBK / 16, kb == 0);
+                        __syncwarp();
+                        ++kb;
+                        if (++s == kStages) { s = 0; ph ^= 1u; }
                     }
-                    steps = (t.k_tail + 15) / 16;
-                    const int from = t.k_tail * 8, to = steps * 16 * 8;  // 16-byte units of a 64-column box
-                    uint4* box = reinterpret_cast<uint4*>(smem + s * kStageBytes);
-                    for (int i = from + lane; i < to; i += 32)
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) box[b * 512 + i] = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (!leader) {
-                        if (lane == 0) arrive_cluster(leader_clear + 8u * s);
-                    } else if (!warp_wait<true>(&clear[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                if (leader) {
-                    if (!warp_wait(&full[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!ok) break;
+                    if (!warp_wait<true>(&tempty[1], want, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
                     tc_fence_after();
                     if (lane == 0) {
-#pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk) {
-                            if (WG && kk >= steps) break;
-                            const uint64_t da = WG ? desc_mn(stage + kk * 2048) : umma_desc_sw128(stage + kk * 32);
-                            const uint64_t db = B_MN ? desc_mn(stage + kOperand + kk * 2048) : umma_desc_sw128(stage + kOperand + kk * 32);
-                            mma_pair(d_tmem, da, db, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        uint32_t st = s0;
+                        for (int b = 0; b < kb; ++b) {
+                            multiply(st, 1, 1, kBK / 16, b == 0);
+                            commit_pair(&empty[st]);
+                            if (++st == kStages) st = 0;
                         }
+                    }
+                    __syncwarp();
+                    (void)ph0;
+                }
+            }
+            const int buf0 = SUB == 1 ? it & 1 : 0;
+            for (; kb < t.kb; ++kb) {
+                const int steps = arrived(t, kb, subs);
+                if (!steps) {
+                    ok = false;
+                    break;
+                }
+                if (leader) {
+                    if (lane == 0) {
+                        for (int j = 0; j < subs; ++j) multiply(s, j, buf0 + j, steps, kb == 0);
                         commit_pair(&empty[s]);
-                        if (kb == t.kb - 1) commit_pair(&tfull[buf]);
                     }
                     __syncwarp();
                 }
                 if (++s == kStages) { s = 0; ph ^= 1u; }
             }
+            if (ok && leader && lane == 0)
+                for (int j = 0; j < subs; ++j) commit_pair(&tfull[buf0 + j]);
+            ++it;
+            uses1 += subs == 2 ? 1u : 0u;
         }
         if (leader && lane == 0) {  // every MMA issued is complete before TMEM is freed
             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
@@ -634,31 +694,44 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         // a quarter take the two column halves.
         const int q = warp & 3, half = (warp - 2) >> 2;
         const uint32_t leader_tempty = peer_addr(smem_u32(tempty), 0);
-        Epilogue<EPI> epi{a, smem + kStages * kStageBytes + (warp - 2) * 4096, lane};
+        Epilogue<EPI> epi{a, smem + kRingBytes + (warp - 2) * kStaging, lane};
         int it = 0;
-        for (int tile = pair; tile < sc.total; tile += npairs) {
+        uint32_t uses1 = 0;
+        bool ok = true;
+        for (int tile = pair; ok && tile < sc.total; tile += npairs) {
             const Tile t = decode<WG>(a, sc, tile);
             const int r0 = static_cast<int>(rank) * 128 + q * 32;  // this warp's first row of the tile
             const int rows = max(0, min(32, (WG ? a.M - t.m * 256 : t.rows) - r0));
             const int64_t row0 = WG ? static_cast<int64_t>(t.g) * a.M + t.m * 256 + r0 : t.row0 + r0;
             const int sel = WG && t.n >= a.n_first ? 1 : 0;
-            const int col0 = (t.n - sel * a.n_first) * (EPI == E_GATE ? 128 : 256) + half * (EPI == E_GATE ? 64 : 128);
-            if (WG && t.kb == 0) {
-                epi.zero(row0, rows, col0, sel);
-                continue;
+            const int tile_col = (t.n - sel * a.n_first) * SUB * kSubCols;
+            const int subs = SUB == 1 ? 1 : min(SUB, (a.N - tile_col + kSubCols - 1) / kSubCols);
+            for (int j = 0; j < subs; ++j) {
+                const int col0 = tile_col + j * kSubCols + half * (kSubCols / 2);
+                if (WG && t.kb == 0) {
+                    epi.zero(row0, rows, col0, sel);
+                    continue;
+                }
+                const int buf = SUB == 1 ? it & 1 : j;
+                const uint32_t use = SUB == 1 ? static_cast<uint32_t>(it >> 1) : (j ? uses1 : static_cast<uint32_t>(it));
+                const bool mine = rows > 0 && col0 < a.N;
+                if (mine) epi.load(row0, rows, col0);
+                if (!warp_wait(&tfull[buf], use & 1u, a, DEV_TIMEOUT_EPI_TFULL, abort_flag, peer_abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t taddr = tmem_base + static_cast<uint32_t>(buf) * 256u + (static_cast<uint32_t>(q * 32) << 16) +
+                                       static_cast<uint32_t>(half * (kSubCols / 2));
+                if (mine) epi.run(taddr, row0, rows, col0, sel);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(leader_tempty + 8u * buf);
             }
-            const int buf = it & 1;
-            const uint32_t use = static_cast<uint32_t>(it >> 1);
-            ++it;
-            if (rows > 0 && col0 < a.N) epi.load(row0, rows, col0);
-            if (!warp_wait(&tfull[buf], use & 1u, a, DEV_TIMEOUT_EPI_TFULL, abort_flag, peer_abort)) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + static_cast<uint32_t>(buf) * 256u + (static_cast<uint32_t>(q * 32) << 16) +
-                                   static_cast<uint32_t>(half * (EPI == E_GATE ? 64 : 128));
-            if (rows > 0) epi.run(taddr, row0, rows, col0, sel);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(leader_tempty + 8u * buf);
+            if (!(WG && t.kb == 0)) {
+                ++it;
+                uses1 += subs == 2 ? 1u : 0u;
+            }
         }
     }
 
@@ -670,12 +743,13 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         // same uses on both sides; after an abort the leader makes up for the
         // difference (at most the ring, since a use waits for its stage).
         const uint32_t mine = issued[0], theirs = issued[2];
+        const uint32_t *my_bytes = issued + 4, *their_bytes = my_bytes + kMaxStages;
         const uint32_t first = mine > kStages ? mine - kStages : 0u;
         for (uint32_t u = theirs > first ? theirs : first; u < mine; ++u)
-            if (!((issued[1] >> (u % kStages)) & 1u)) mbar_complete_tx(&full[u % kStages], kStageBytes);
+            if (!((issued[1] >> (u % kStages)) & 1u)) mbar_complete_tx(&full[u % kStages], my_bytes[u % kStages]);
         for (uint32_t u = mine; u < theirs && u < mine + kStages; ++u) {
             if ((issued[3] >> (u % kStages)) & 1u) mbar_arrive(&full[u % kStages]);
-            else mbar_arrive_expect_tx(&full[u % kStages], kStageBytes);
+            else mbar_arrive_expect_tx(&full[u % kStages], their_bytes[u % kStages]);
         }
         const uint32_t last = theirs > mine ? theirs : mine;
         for (uint32_t u = last > kStages ? last - kStages : 0u; u < last; ++u)
@@ -726,28 +800,46 @@ bool map_weights(CUtensorMap* m, const bf16* base, int64_t mats, int64_t rows, i
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * 4096 + (4 * kStages + 5) * 8 + 24 + 2 * (kMaxGroups + 1) * 4;
+constexpr size_t kSmem = 1024 + kRingBytes + kEpiWarps * kStaging + (4 * kMaxStages + 5) * 8 + 8 +
+                         (4 + 2 * kMaxStages) * 4 + 2 * (kMaxGroups + 1) * 4;
 
-template <int EPI, bool B_MN>
-int launch(const Maps& maps, Args a, int max_pairs, cudaStream_t st) {
+template <int EPI, bool B_MN, int SUB>
+int launch_sub(const Maps& maps, Args a, int64_t max_tiles, cudaStream_t st) {
     static std::atomic<unsigned long long> attr_done{0};
-    if (a.G < 1 || a.G > kMaxGroups) return -2;
-    const auto kernel = train_gemm_kernel<EPI, B_MN>;
+    const auto kernel = train_gemm_kernel<EPI, B_MN, SUB>;
     if (smem_attr_once(reinterpret_cast<const void*>(kernel), static_cast<int>(kSmem), attr_done) != 0) return -3;
-    const uint32_t limit = wait_settings().wait_limit;
-    a.wait_limit = limit ? limit : kWaitLimit;
     int pairs = num_sms() / 2;
     if (pairs < 1) return -3;
-    if (pairs > max_pairs) pairs = max_pairs;
+    if (pairs > max_tiles) pairs = static_cast<int>(max_tiles);
     kernel<<<2 * pairs, kThreads, kSmem, st>>>(maps, a);
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
-// Upper bound of a token-major launch's tiles: a group's last tile may be partial.
-int tile_bound(int64_t rows, int G, int n_tiles) {
-    const int64_t t = ((rows + 255) / 256 + G) * n_tiles;
-    return t > (1 << 20) ? (1 << 20) : static_cast<int>(t);
+// K-blocks of a tile from which it takes two sub-tiles.  The epilogue that the
+// next tile then waits for has to be a small part of it; it is longest where
+// it reads the saved projections too, and longer with three outputs.  Two
+// sub-tiles against one, ms: down (224 k-blocks) 2.88, 3.26; dx (448) 5.30,
+// 6.40, (44) 0.299, 0.312; weight gradients (64) 6.65, 8.33, (7) 0.47, 0.44;
+// gate (64) 6.46, 6.68; dgate (64) 4.01, 3.63, (32) 0.263, 0.204.
+constexpr int wide_from(int epi) { return epi == E_DGATE ? 128 : (epi == E_GATE ? 64 : 32); }
+
+// `kb`: k-blocks of a tile (of an average one, for weight gradients); `row_tiles`:
+// an upper bound of the row tiles of all groups; `outs`: outputs side by side.
+template <int EPI, bool B_MN>
+int launch(const Maps& maps, Args a, int kb, int64_t row_tiles, int outs, cudaStream_t st) {
+    if (a.G < 1 || a.G > kMaxGroups) return -2;
+    const uint32_t limit = wait_settings().wait_limit;
+    a.wait_limit = limit ? limit : kWaitLimit;
+    const int sub_cols = EPI == E_GATE ? 128 : 256;
+    const int sub = kb >= wide_from(EPI) ? 2 : 1;
+    a.n_first = ceil_div(a.N, sub * sub_cols);
+    a.n_tiles = outs * a.n_first;
+    return sub == 2 ? launch_sub<EPI, B_MN, 2>(maps, a, row_tiles * a.n_tiles, st)
+                    : launch_sub<EPI, B_MN, 1>(maps, a, row_tiles * a.n_tiles, st);
 }
+
+// Upper bound of a token-major launch's row tiles: a group's last one may be partial.
+int64_t row_tile_bound(int64_t rows, int G) { return (rows + 255) / 256 + G; }
 
 }  // namespace
 
@@ -764,13 +856,12 @@ int launch_train_gate(const bf16* x, const int32_t* off, int64_t rows, int E, in
     a.cap = rows;
     a.G = E;
     a.N = f;
-    a.n_tiles = ceil_div(f, 128);
     a.kb_first = a.kb_all = ceil_div(d, kBK);
     a.ld = 2 * static_cast<int64_t>(f);
     a.out[0] = gu;
     a.h = h;
     a.status = status;
-    return launch<E_GATE, true>(m, a, tile_bound(rows, E, a.n_tiles), st);
+    return launch<E_GATE, true>(m, a, a.kb_all, row_tile_bound(rows, E), 1, st);
 }
 
 int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2, float* y,
@@ -785,12 +876,11 @@ int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, in
     a.cap = rows;
     a.G = E;
     a.N = d;
-    a.n_tiles = ceil_div(d, 256);
     a.kb_first = a.kb_all = ceil_div(f, kBK);
     a.ld = d;
     a.out[0] = y;
     a.status = status;
-    return launch<E_F32, true>(m, a, tile_bound(rows, E, a.n_tiles), st);
+    return launch<E_F32, true>(m, a, a.kb_all, row_tile_bound(rows, E), 1, st);
 }
 
 int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2,
@@ -805,13 +895,12 @@ int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, 
     a.cap = rows;
     a.G = E;
     a.N = f;
-    a.n_tiles = ceil_div(f, 256);
     a.kb_first = a.kb_all = ceil_div(d, kBK);
     a.ld = 2 * static_cast<int64_t>(f);
     a.out[0] = dgu;
     a.gu = gu;
     a.status = status;
-    return launch<E_DGATE, false>(m, a, tile_bound(rows, E, a.n_tiles), st);
+    return launch<E_DGATE, false>(m, a, a.kb_all, row_tile_bound(rows, E), 1, st);
 }
 
 int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W1,
@@ -827,13 +916,12 @@ int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, in
     a.cap = rows;
     a.G = E;
     a.N = d;
-    a.n_tiles = ceil_div(d, 256);
     a.kb_first = ceil_div(f, kBK);
     a.kb_all = 2 * a.kb_first;
     a.ld = d;
     a.out[0] = dx;
     a.status = status;
-    return launch<E_BF16, false>(m, a, tile_bound(rows, E, a.n_tiles), st);
+    return launch<E_BF16, false>(m, a, a.kb_all, row_tile_bound(rows, E), 1, st);
 }
 
 int launch_train_dw(const bf16* left, int m_cols, const bf16* right0, const bf16* right1, int64_t right_ld, int n_cols,
@@ -854,15 +942,13 @@ int launch_train_dw(const bf16* left, int m_cols, const bf16* right0, const bf16
     a.M = m_cols;
     a.N = n_cols;
     a.m_tiles = ceil_div(m_cols, 256);
-    a.n_first = ceil_div(n_cols, 256);
-    a.n_tiles = (right1 ? 2 : 1) * a.n_first;
     a.ld = out_ld;
     a.out[0] = out0;
     a.out[1] = out1;
     a.out_bf16 = out_bf16 ? 1 : 0;
     a.status = status;
-    const int64_t tiles = static_cast<int64_t>(G) * a.m_tiles * a.n_tiles;
-    return launch<E_WGRAD, true>(m, a, tiles > (1 << 20) ? (1 << 20) : static_cast<int>(tiles), st);
+    const int kb = ceil_div(off ? rows / G : chunk, kBK);
+    return launch<E_WGRAD, true>(m, a, kb, static_cast<int64_t>(G) * a.m_tiles, right1 ? 2 : 1, st);
 }
 
 }  // namespace moe
