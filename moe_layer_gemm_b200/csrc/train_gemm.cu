@@ -35,7 +35,7 @@
 //   tfull[b]   both: the leader's MMA commit arrives on both
 //   tempty[b]  leader: all epilogue warps of the pair arrive
 //   tail[s]    both: a CTA's own loads of a k-block that its group ends in
-//   clear[s]   leader: the peer has cleared the rows behind the group
+//   clear[s]   leader: both CTAs have cleared the rows behind the group
 // Only full[] and empty[] are used per k-block, and nothing a k-block waits
 // for goes through the peer's threads: with each CTA's loads on its own full[]
 // and a thread of the peer passing the news on, a release-arrive a k-block
@@ -65,7 +65,8 @@ constexpr uint32_t kRingBytes = 12 * kOperand;
 constexpr int kStaging = 2048;  // per epilogue warp
 constexpr uint32_t kTmemCols = 512;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 64 + 32 * kEpiWarps;   // weight gradients: one more warp, which clears tails
+constexpr int kClearWarp = 2 + kEpiWarps;
 constexpr int kMaxGroups = 256;
 constexpr int kMaxStages = 6;
 constexpr int kRaster = 3;  // tile columns walked together: the operands of the ~74 tiles in flight stay in L2
@@ -423,7 +424,7 @@ struct Epilogue {
 // epilogue, except that up to a ring of its k-blocks are multiplied into the
 // first accumulator while the second is still being read.
 template <int EPI, bool B_MN, int SUB>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EPI == E_WGRAD ? kThreads + 32 : kThreads, 1)
 train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     constexpr bool WG = EPI == E_WGRAD;
     constexpr uint32_t kStageBytes = (1 + SUB) * kOperand;
@@ -452,7 +453,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&tail[s], 1);
-            mbar_init(&clear[s], 1);
+            mbar_init(&clear[s], 2);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
@@ -472,7 +473,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     // Offsets clamped to the matrices' rows: no value in the array is ever an address.
-    for (int g = threadIdx.x; g <= a.G; g += kThreads) {
+    for (int g = threadIdx.x; g <= a.G; g += blockDim.x) {
         const int64_t o = a.off != nullptr ? static_cast<int64_t>(a.off[g]) : static_cast<int64_t>(g) * a.chunk;
         off[g] = static_cast<int>(o < 0 ? 0 : (o > a.cap ? a.cap : o));
     }
@@ -575,35 +576,23 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 for (int i = 0; i < kStages; ++i) store_cluster(rec + 4u * (4 + kMaxStages + i), use_bytes[i]);
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer (leader); the peer only clears tails
+        // ---------------------------------------------------- MMA issuer (leader)
         // idesc: D fp32, A and B bf16, bits 15 and 16 set where A, B are M-, N-contiguous
         constexpr uint32_t idesc = umma_idesc_bf16(256, 256) | (WG ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
-        const uint32_t leader_clear = peer_addr(smem_u32(clear), 0);
         uint32_t s = 0, ph = 0, tail_ph = 0, uses1 = 0;  // uses1: tiles that filled the second of two sub-tiles
         int it = 0;
         bool ok = true;
-        // Wait until k-block kb of the tile is in stage s of both CTAs, a
-        // tail's rows behind the group cleared; the 16-k steps to multiply, 0: abort.
-        auto arrived = [&](const Tile& t, int kb, int subs) -> int {
+        // Wait until k-block kb of the tile is in stage s of both CTAs, a tail's
+        // rows behind the group cleared; the 16-k steps to multiply, 0: abort.
+        auto arrived = [&](const Tile& t, int kb) -> int {
             int steps = kBK / 16;
             if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
                 const uint32_t tph = (tail_ph >> s) & 1u;
                 tail_ph ^= 1u << s;
-                if (!warp_wait(&tail[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
+                if (!warp_wait<true>(&clear[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
                 steps = (t.k_tail + 15) / 16;
-                const int from = t.k_tail * 8, to = steps * 16 * 8;  // 16-byte units of a 64-column box
-                uint4* box = reinterpret_cast<uint4*>(smem + s * kStageBytes);
-                for (int i = from + lane; i < to; i += 32)
-                    for (int b = 0; b < 2 + 2 * subs; ++b) box[b * 512 + i] = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (!leader) {
-                    if (lane == 0) arrive_cluster(leader_clear + 8u * s);
-                } else if (!warp_wait<true>(&clear[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) {
-                    return 0;
-                }
             }
-            if (leader && !warp_wait(&full[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
+            if (!warp_wait(&full[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
             tc_fence_after();
             return steps;
         };
@@ -619,65 +608,57 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 mma_pair(d_tmem, da, db, idesc, (!first || kk > 0) ? 1u : 0u);
             }
         };
-        for (int tile = pair; ok && (WG || leader) && tile < sc.total; tile += npairs) {
+        for (int tile = pair; ok && leader && tile < sc.total; tile += npairs) {
             const Tile t = decode<WG>(a, sc, tile);
             if (t.kb == 0) continue;
             const int col0 = (t.n - (WG && t.n >= a.n_first ? a.n_first : 0)) * SUB * kSubCols;
             const int subs = SUB == 1 ? 1 : min(SUB, (a.N - col0 + kSubCols - 1) / kSubCols);
             int kb = 0;
-            if (leader) {
-                const int buf = SUB == 1 ? it & 1 : 0;
-                const uint32_t use = static_cast<uint32_t>(SUB == 1 ? it >> 1 : it);
-                if (!warp_wait<true>(&tempty[buf], (use & 1u) ^ 1u, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
-                tc_fence_after();
-                if (SUB == 2 && subs == 2) {
-                    // the second accumulator may still be read: go ahead in the first
-                    // with the k-blocks that the ring holds (whole ones, before any tail)
-                    const uint32_t s0 = s, ph0 = ph;
-                    const uint32_t want = (uses1 & 1u) ^ 1u;
-                    while (kb < kStages && kb < t.kb - 1) {
-                        if (__all_sync(0xffffffffu, try_wait_cluster(&tempty[1], want))) break;
-                        if (!arrived(t, kb, subs)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) multiply(s, 0, 0, kBK / 16, kb == 0);
-                        __syncwarp();
-                        ++kb;
-                        if (++s == kStages) { s = 0; ph ^= 1u; }
-                    }
-                    if (!ok) break;
-                    if (!warp_wait<true>(&tempty[1], want, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        uint32_t st = s0;
-                        for (int b = 0; b < kb; ++b) {
-                            multiply(st, 1, 1, kBK / 16, b == 0);
-                            commit_pair(&empty[st]);
-                            if (++st == kStages) st = 0;
-                        }
-                    }
-                    __syncwarp();
-                    (void)ph0;
-                }
-            }
             const int buf0 = SUB == 1 ? it & 1 : 0;
+            const uint32_t use = static_cast<uint32_t>(SUB == 1 ? it >> 1 : it);
+            if (!warp_wait<true>(&tempty[buf0], (use & 1u) ^ 1u, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
+            tc_fence_after();
+            if (SUB == 2 && subs == 2) {
+                // the second accumulator may still be read: go ahead in the first
+                // with the k-blocks that the ring holds (whole ones, before any tail)
+                const uint32_t s0 = s, want = (uses1 & 1u) ^ 1u;
+                while (kb < kStages && kb < t.kb - 1) {
+                    if (__all_sync(0xffffffffu, try_wait_cluster(&tempty[1], want))) break;
+                    if (!arrived(t, kb)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) multiply(s, 0, 0, kBK / 16, kb == 0);
+                    __syncwarp();
+                    ++kb;
+                    if (++s == kStages) { s = 0; ph ^= 1u; }
+                }
+                if (!ok || !warp_wait<true>(&tempty[1], want, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    uint32_t st = s0;
+                    for (int b = 0; b < kb; ++b) {
+                        multiply(st, 1, 1, kBK / 16, b == 0);
+                        commit_pair(&empty[st]);
+                        if (++st == kStages) st = 0;
+                    }
+                }
+                __syncwarp();
+            }
             for (; kb < t.kb; ++kb) {
-                const int steps = arrived(t, kb, subs);
+                const int steps = arrived(t, kb);
                 if (!steps) {
                     ok = false;
                     break;
                 }
-                if (leader) {
-                    if (lane == 0) {
-                        for (int j = 0; j < subs; ++j) multiply(s, j, buf0 + j, steps, kb == 0);
-                        commit_pair(&empty[s]);
-                    }
-                    __syncwarp();
+                if (lane == 0) {
+                    for (int j = 0; j < subs; ++j) multiply(s, j, buf0 + j, steps, kb == 0);
+                    commit_pair(&empty[s]);
                 }
+                __syncwarp();
                 if (++s == kStages) { s = 0; ph ^= 1u; }
             }
-            if (ok && leader && lane == 0)
+            if (ok && lane == 0)
                 for (int j = 0; j < subs; ++j) commit_pair(&tfull[buf0 + j]);
             ++it;
             uses1 += subs == 2 ? 1u : 0u;
@@ -688,6 +669,31 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             mbar_drain(drain, 0, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
         }
         __syncwarp();
+    } else if (WG && warp == kClearWarp) {
+        // ---------------------------------------------------- tails (both CTAs)
+        // A group ends inside a tile's last box: clear the rows behind it, up to
+        // the last 16-row step that is multiplied, once the box has landed.
+        const uint32_t leader_clear = peer_addr(smem_u32(clear), 0);
+        uint32_t s = 0, tail_ph = 0;
+        for (int tile = pair; tile < sc.total; tile += npairs) {
+            const Tile t = decode<WG>(a, sc, tile);
+            if (t.kb == 0) continue;
+            s = (s + static_cast<uint32_t>(t.kb)) % kStages;
+            if (t.k_tail == kBK) continue;
+            const uint32_t st = (s + kStages - 1) % kStages;
+            const uint32_t tph = (tail_ph >> st) & 1u;
+            tail_ph ^= 1u << st;
+            if (!warp_wait(&tail[st], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) break;
+            const int col0 = (t.n - (t.n >= a.n_first ? a.n_first : 0)) * SUB * kSubCols;
+            const int subs = SUB == 1 ? 1 : min(SUB, (a.N - col0 + kSubCols - 1) / kSubCols);
+            const int from = t.k_tail * 8, to = (t.k_tail + 15) / 16 * 128;  // 16-byte units of a 64-column box
+            uint4* box = reinterpret_cast<uint4*>(smem + st * kStageBytes);
+            for (int i = from + lane; i < to; i += 32)
+                for (int b = 0; b < 2 + 2 * subs; ++b) box[b * 512 + i] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(leader_clear + 8u * st);
+        }
     } else {
         // ---------------------------------------------------- epilogue (both CTAs)
         // Warp quarter q holds rows 32 q .. of this CTA's 128; the two warps of
@@ -811,7 +817,7 @@ int launch_sub(const Maps& maps, Args a, int64_t max_tiles, cudaStream_t st) {
     int pairs = num_sms() / 2;
     if (pairs < 1) return -3;
     if (pairs > max_tiles) pairs = static_cast<int>(max_tiles);
-    kernel<<<2 * pairs, kThreads, kSmem, st>>>(maps, a);
+    kernel<<<2 * pairs, EPI == E_WGRAD ? kThreads + 32 : kThreads, kSmem, st>>>(maps, a);
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 
