@@ -837,7 +837,7 @@ int launch(const Maps& maps, Args a, int kb, int64_t row_tiles, int outs, cudaSt
     const uint32_t limit = wait_settings().wait_limit;
     a.wait_limit = limit ? limit : kWaitLimit;
     const int sub_cols = EPI == E_GATE ? 128 : 256;
-    const int sub = kb >= wide_from(EPI) ? 2 : 1;
+    const int sub = kb >= wide_from(EPI) && a.N > sub_cols ? 2 : 1;
     a.n_first = ceil_div(a.N, sub * sub_cols);
     a.n_tiles = outs * a.n_first;
     return sub == 2 ? launch_sub<EPI, B_MN, 2>(maps, a, row_tiles * a.n_tiles, st)
