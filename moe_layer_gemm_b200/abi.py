@@ -425,13 +425,18 @@ def moe_expert_ffn_slots(dims, x_perm, offsets, expert_slot, n_slots: int, W13c,
 
 # ---------------------------------------------------------------- training
 
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
 class _On:
-    """Checks one call's tensors and launches it on their device and stream."""
+    """Checks one call's tensors and launches it on their device and its current stream."""
+
+    __slots__ = ("index", "stream")
 
     def __init__(self, anchor, stream):
-        if not isinstance(anchor, torch.Tensor) or anchor.device.type != "cuda":
+        if not isinstance(anchor, torch.Tensor) or not anchor.is_cuda:
             raise ValueError("expected CUDA tensors")
-        self.device, self.stream = anchor.device, stream
+        self.index, self.stream = anchor.get_device(), stream
 
     def ptr(self, t, numel: int, name: str, dtype=None, optional: bool = False):
         """Address of a contiguous tensor of at least `numel` values on the call's device."""
@@ -439,9 +444,11 @@ class _On:
             if optional:
                 return None
             raise ValueError(f"{name}: required")
+        if type(t) is torch.Tensor and t.dtype == (dtype or t.dtype) and t.get_device() == self.index and t.numel() >= numel and t.is_contiguous():
+            return t.data_ptr()
         p = _ptr(t, dtype, name)
-        if t.device != self.device:
-            raise ValueError(f"{name}: on {t.device}, the call's other tensors are on {self.device}")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name}: on {t.device}, the call's other tensors are on cuda:{self.index}")
         if t.numel() < numel:
             raise ValueError(f"{name}: {t.numel()} values, {numel} needed")
         return p
@@ -455,15 +462,19 @@ class _On:
         return self.ptr(t, numel, name, None if like is None else like.dtype, optional), int(t is not None and t.dtype == BF16)
 
     def call(self, name: str, *args):
-        fn = getattr(load(), name)
-        if torch.cuda.current_device() == self.device.index:
-            _check(name, fn(*args, self._stream()))
+        fn = getattr(_lib or load(), name)
+        if torch.cuda.current_device() == self.index:
+            status = fn(*args, self._stream())
         else:
-            with torch.cuda.device(self.device):
-                _check(name, fn(*args, self._stream()))
+            with torch.cuda.device(self.index):
+                status = fn(*args, self._stream())
+        if status != MOE_OK:
+            _check(name, status)
 
     def _stream(self):
-        return torch.cuda.current_stream(self.device).cuda_stream if self.stream is None else _stream(self.stream)
+        if self.stream is not None:
+            return _stream(self.stream)
+        return _raw_stream(self.index) if _raw_stream is not None else torch.cuda.current_stream(self.index).cuda_stream
 
 
 def _rows_of(x, name):

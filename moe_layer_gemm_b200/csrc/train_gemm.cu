@@ -90,6 +90,7 @@ struct Args {
     int out_bf16;          // E_WGRAD: bf16 output, else fp32
     int* status;
     uint32_t wait_limit;
+    int never_ready;  // a test of the timeout paths: the epilogue waits for what nothing completes
 };
 
 struct Maps {
@@ -107,9 +108,8 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));
     return out;
 }
-__device__ __forceinline__ void pair_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void pair_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void pair_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void store_cluster(uint32_t cluster_addr, uint32_t v) {
     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
@@ -439,7 +439,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     uint64_t* tfull = clear + kStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* never = drain + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     uint32_t* issued = tmem_slot + 2;  // [rank][stage uses issued, stages whose last use was a tail], [rank][use_bytes]
     int* off = reinterpret_cast<int*>(issued + 4 + 2 * kMaxStages);
@@ -460,6 +461,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             mbar_init(&tempty[b], 2 * kEpiWarps);
         }
         mbar_init(drain, 1);
+        mbar_init(never, 1);
         *abort_flag = 0;
         fence_mbar_init();
         for (int i = 0; i < 2; ++i) {
@@ -472,6 +474,12 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                      ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    __syncwarp();
+    pair_arrive();  // this CTA's barriers exist; the other's are waited for below
+    // Under programmatic launch all of the above ran while the previous kernel
+    // of the stream finished; the next one may do the same from here on.
+    pdl_wait();
+    pdl_trigger();
     // Offsets clamped to the matrices' rows: no value in the array is ever an address.
     for (int g = threadIdx.x; g <= a.G; g += blockDim.x) {
         const int64_t o = a.off != nullptr ? static_cast<int64_t>(a.off[g]) : static_cast<int64_t>(g) * a.chunk;
@@ -497,7 +505,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     }
     tc_fence_before();
     __syncthreads();
-    pair_sync();
+    pair_wait();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const Sched sc{off, start, start[a.G]};
@@ -722,7 +730,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 const uint32_t use = SUB == 1 ? static_cast<uint32_t>(it >> 1) : (j ? uses1 : static_cast<uint32_t>(it));
                 const bool mine = rows > 0 && col0 < a.N;
                 if (mine) epi.load(row0, rows, col0);
-                if (!warp_wait(&tfull[buf], use & 1u, a, DEV_TIMEOUT_EPI_TFULL, abort_flag, peer_abort)) {
+                if (!warp_wait(a.never_ready ? never : &tfull[buf], a.never_ready ? 0u : use & 1u, a, DEV_TIMEOUT_EPI_TFULL, abort_flag,
+                               peer_abort)) {
                     ok = false;
                     break;
                 }
@@ -741,13 +750,11 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         }
     }
 
-    tc_fence_before();
-    __syncthreads();
-    pair_sync();  // all roles of both CTAs have stopped
-    if (leader && threadIdx.x == 0) {
-        // No copy is in flight when the pair ends.  A complete run issued the
-        // same uses on both sides; after an abort the leader makes up for the
-        // difference (at most the ring, since a use waits for its stage).
+    // No copy is in flight when the pair ends.  A complete run issued the same
+    // uses on both sides and multiplied them all; after an abort the leader
+    // makes up for the difference (at most the ring, since a use waits for its
+    // stage) and waits for what was issued.
+    auto reconcile = [&]() {
         const uint32_t mine = issued[0], theirs = issued[2];
         const uint32_t *my_bytes = issued + 4, *their_bytes = my_bytes + kMaxStages;
         const uint32_t first = mine > kStages ? mine - kStages : 0u;
@@ -760,9 +767,19 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         const uint32_t last = theirs > mine ? theirs : mine;
         for (uint32_t u = last > kStages ? last - kStages : 0u; u < last; ++u)
             mbar_drain(&full[u % kStages], (u / kStages) & 1u, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
-    }
+    };
+    tc_fence_before();
     __syncthreads();
-    pair_sync();  // neither CTA's memory goes while the other may still use it
+    // All roles of both CTAs have stopped; neither CTA's memory goes while the
+    // other may still use it.
+    pair_arrive();
+    pair_wait();
+    if (*abort_flag) {  // raised in both CTAs or in neither: whoever raised it told both before this barrier
+        if (leader && threadIdx.x == 0) reconcile();
+        __syncthreads();
+        pair_arrive();
+        pair_wait();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
@@ -806,7 +823,7 @@ bool map_weights(CUtensorMap* m, const bf16* base, int64_t mats, int64_t rows, i
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-constexpr size_t kSmem = 1024 + kRingBytes + kEpiWarps * kStaging + (4 * kMaxStages + 5) * 8 + 8 +
+constexpr size_t kSmem = 1024 + kRingBytes + kEpiWarps * kStaging + (4 * kMaxStages + 6) * 8 + 8 +
                          (4 + 2 * kMaxStages) * 4 + 2 * (kMaxGroups + 1) * 4;
 
 template <int EPI, bool B_MN, int SUB>
@@ -817,8 +834,19 @@ int launch_sub(const Maps& maps, Args a, int64_t max_tiles, cudaStream_t st) {
     int pairs = num_sms() / 2;
     if (pairs < 1) return -3;
     if (pairs > max_tiles) pairs = static_cast<int>(max_tiles);
-    kernel<<<2 * pairs, EPI == E_WGRAD ? kThreads + 32 : kThreads, kSmem, st>>>(maps, a);
-    return cudaGetLastError() == cudaSuccess ? 0 : -3;
+    // Programmatic launch: where the tiles are few, the set-up of one product's
+    // kernel runs on free SMs under the previous product's end.
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(EPI == E_WGRAD ? kThreads + 32 : kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, a) == cudaSuccess ? 0 : -3;
 }
 
 // K-blocks of a tile from which it takes two sub-tiles.  The epilogue that the
@@ -834,8 +862,9 @@ constexpr int wide_from(int epi) { return epi == E_DGATE ? 128 : (epi == E_GATE 
 template <int EPI, bool B_MN>
 int launch(const Maps& maps, Args a, int kb, int64_t row_tiles, int outs, cudaStream_t st) {
     if (a.G < 1 || a.G > kMaxGroups) return -2;
-    const uint32_t limit = wait_settings().wait_limit;
-    a.wait_limit = limit ? limit : kWaitLimit;
+    const WaitSettings wt = wait_settings();
+    a.wait_limit = wt.wait_limit ? wt.wait_limit : kWaitLimit;
+    a.never_ready = wt.dep_never_ready;
     const int sub_cols = EPI == E_GATE ? 128 : 256;
     const int sub = kb >= wide_from(EPI) && a.N > sub_cols ? 2 : 1;
     a.n_first = ceil_div(a.N, sub * sub_cols);

@@ -169,6 +169,11 @@ FFN = [  # T, d, f, E, K, drop, empty experts
     (777, 1024, 528, 60, 4, 0.25, (5, 6, 59)),
     (2100, 320, 256, 1, 1, 0.0, ()),
     (500, 64, 64, 256, 8, 0.0, ()),
+    # reductions long enough for tiles of two sub-tiles: the gate product's, the saved projections' gradient's, the weights'
+    (40, 4112, 400, 2, 1, 0.0, ()),
+    (30, 8208, 528, 1, 1, 0.0, ()),
+    (4300, 320, 784, 2, 1, 0.0, ()),
+    (4200, 800, 80, 2, 2, 0.3, ()),
 ]
 
 
