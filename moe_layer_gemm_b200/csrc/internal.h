@@ -232,10 +232,18 @@ int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, 
                        const bf16* gu, bf16* dgu, int* status, cudaStream_t st);
 int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W1,
                     const bf16* W3, bf16* dx, int* status, cudaStream_t st);
-// out_j[g] = left[rows of g]^T right_j[rows of g]; groups by offsets, or of `chunk` rows when off is nullptr.
-int launch_train_dw(const bf16* left, int m_cols, const bf16* right0, const bf16* right1, int64_t right_ld, int n_cols,
-                    const int32_t* off, int64_t chunk, int64_t rows, int G, void* out0, void* out1, int64_t out_ld,
-                    bool out_bf16, int* status, cudaStream_t st);
+// out[g] = left[rows of g]^T right[rows of g], [M, N], for up to 3 pairs in one
+// launch; groups by offsets, or of `chunk` rows when off is nullptr.
+struct WeightGradient {
+    const bf16* left;  // [rows, M]
+    int M;
+    const bf16* right;  // [rows, N] with rows of right_ld elements
+    int N;
+    int64_t right_ld;
+    void* out;  // [G, M, N]
+};
+int launch_train_dw(const WeightGradient* w, int n, const int32_t* off, int64_t chunk, int64_t rows, int G, bool out_bf16,
+                    int* status, cudaStream_t st);
 
 // ------------------------------------------------------------ training: around the experts (train.cu)
 int launch_combine_backward(const void* dy, bool dy_bf16, const float* y_perm, const int32_t* inv, const float* w, int64_t T,

@@ -132,15 +132,17 @@ int moe_ffn_backward(const moe_dims* dims, const moe_bf16* dy_perm, const moe_bf
     const int E = dims->E, d = dims->d_model, f = dims->d_ff;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int* status = static_cast<int*>(ws);
-    const bool b = dw_is_bf16 != 0;
     MOE_TRY(map_launch(launch_train_dgate(in16(dy_perm), offsets, A, E, d, f, in16(W2), in16(gu), out16(dgu), status, st)));
     if (dx_perm)
         MOE_TRY(map_launch(launch_train_dx(out16(dgu), offsets, A, E, d, f, in16(W1), in16(W3), out16(dx_perm), status, st)));
-    if (dW1)
-        MOE_TRY(map_launch(launch_train_dw(in16(x_perm), d, out16(dgu), out16(dgu) + f, 2 * static_cast<int64_t>(f), f, offsets, 0, A,
-                                           E, dW1, dW3, f, b, status, st)));
-    if (dW2)
-        MOE_TRY(map_launch(launch_train_dw(in16(h), f, in16(dy_perm), nullptr, d, d, offsets, 0, A, E, dW2, nullptr, d, b, status, st)));
+    WeightGradient w[3];
+    int n = 0;
+    if (dW1) {
+        w[n++] = {in16(x_perm), d, out16(dgu), f, 2 * static_cast<int64_t>(f), dW1};
+        w[n++] = {in16(x_perm), d, out16(dgu) + f, f, 2 * static_cast<int64_t>(f), dW3};
+    }
+    if (dW2) w[n++] = {in16(h), f, in16(dy_perm), d, d, dW2};
+    if (n > 0) MOE_TRY(map_launch(launch_train_dw(w, n, offsets, 0, A, E, dw_is_bf16 != 0, status, st)));
     return MOE_OK;
 }
 
@@ -202,8 +204,8 @@ int moe_route_backward(const moe_dims* dims, const moe_bf16* x, const moe_bf16* 
     }
     if (dWr) {
         float* part = reinterpret_cast<float*>(base + L.part);
-        MOE_TRY(map_launch(launch_train_dw(in16(x), d, dl, nullptr, L.ld, L.ld, nullptr, L.chunk, T, L.S, part, nullptr, L.ld, false,
-                                           status, st)));
+        const WeightGradient w{in16(x), d, dl, L.ld, L.ld, part};
+        MOE_TRY(map_launch(launch_train_dw(&w, 1, nullptr, L.chunk, T, L.S, false, status, st)));
         MOE_TRY(map_launch(launch_router_weight(part, L.S, d, E, L.ld, dWr, dw_is_bf16 != 0, st)));
     }
     return MOE_OK;

@@ -8,8 +8,7 @@
 //   down    Y = H W2
 //   dgate   dH = dY W2^T, then dG, dU from dH, G, U    (one launch)
 //   dx      dX = dG W1^T + dU W3^T                     (one accumulation)
-//   dw13    dW1 = X^T dG, dW3 = X^T dU                 (one launch)
-//   dw2     dW2 = H^T dY
+//   dw      dW1 = X^T dG, dW3 = X^T dU, dW2 = H^T dY   (one launch)
 // and for the router, with dL [T, E] the logits' gradients:
 //   router dw   dWr = x^T dL                           (token chunks as groups)
 //
@@ -73,18 +72,24 @@ constexpr int kRaster = 3;  // tile columns walked together: the operands of the
 
 enum Epi : int { E_GATE, E_F32, E_DGATE, E_BF16, E_WGRAD };
 
+// A weight gradient [M, N] of every group, rows of ld elements.
+struct Product {
+    int M, N;
+    int m_tiles, n_tiles;
+    int64_t ld;
+    void* out;
+};
+constexpr int kProducts = 3;
+
 struct Args {
     const int32_t* off;  // [G + 1] group offsets, or nullptr: groups of `chunk` rows
     int64_t cap;         // rows of the token matrices
     int64_t chunk;
     int G;
-    int M;             // weight gradients: output rows of a group
-    int N;             // output columns (E_GATE: of each projection)
-    int n_tiles, m_tiles;  // column tiles (of SUB sub-tiles), row tiles of a weight gradient
-    int kb_first, kb_all;  // k-blocks of the first operand pair, and of both (token-major products)
-    int n_first;           // weight gradients: column tiles of the first output
-    int64_t ld;            // output row stride
-    void* out[2];
+    int kb_first, kb_all;  // token-major: k-blocks of the first operand pair, and of both
+    Product p[kProducts];  // weight gradients: `products` of them; token-major: p[0] without rows
+    int products;
+    int group_tiles;       // weight gradients: tiles of a group, all products
     bf16* h;               // E_GATE: activations out
     const bf16* gu;        // E_DGATE: saved projections [rows, 2 N]
     int out_bf16;          // E_WGRAD: bf16 output, else fp32
@@ -94,8 +99,8 @@ struct Args {
 };
 
 struct Maps {
-    CUtensorMap a[2];
-    CUtensorMap b[2];
+    CUtensorMap a[kProducts];
+    CUtensorMap b[kProducts];
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -161,7 +166,7 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
 }
 
 struct Tile {
-    int g, n, m;       // group, column tile, row tile
+    int g, j, n, m;    // group, product, column tile, row tile
     int64_t row0;      // token-major: first token row; weight gradient: first row of the reduction
     int rows;          // token-major: valid rows of the tile (<= 256)
     int kb;            // k-blocks
@@ -177,27 +182,36 @@ struct Sched {
 template <bool WG>
 __device__ __forceinline__ Tile decode(const Args& a, const Sched& sc, int tile) {
     Tile t;
-    int lo = 0, hi = a.G;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sc.start[mid] <= tile) lo = mid; else hi = mid;
+    int local;
+    t.j = 0;
+    if (WG) {
+        t.g = tile / a.group_tiles;
+        local = tile - t.g * a.group_tiles;
+        for (int n; t.j + 1 < a.products && local >= (n = a.p[t.j].m_tiles * a.p[t.j].n_tiles); ++t.j) local -= n;
+    } else {
+        int lo = 0, hi = a.G;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sc.start[mid] <= tile) lo = mid; else hi = mid;
+        }
+        t.g = lo;
+        local = tile - sc.start[lo];
     }
-    t.g = lo;
-    const int local = tile - sc.start[lo];
-    const int rows = max(0, sc.off[lo + 1] - sc.off[lo]);
-    const int mt = WG ? a.m_tiles : (rows + 255) >> 8;
+    const Product& p = a.p[t.j];
+    const int rows = max(0, sc.off[t.g + 1] - sc.off[t.g]);
+    const int mt = WG ? p.m_tiles : (rows + 255) >> 8;
     const int band = local / (mt * kRaster);
-    const int width = min(kRaster, a.n_tiles - band * kRaster);
+    const int width = min(kRaster, p.n_tiles - band * kRaster);
     const int in = local - band * kRaster * mt;
     t.m = in / width;
     t.n = band * kRaster + in - t.m * width;
     if (WG) {
-        t.row0 = sc.off[lo];
+        t.row0 = sc.off[t.g];
         t.rows = 256;
         t.kb = (rows + kBK - 1) / kBK;
         t.k_tail = rows - (t.kb - 1) * kBK;
     } else {
-        t.row0 = sc.off[lo] + t.m * 256;
+        t.row0 = sc.off[t.g] + t.m * 256;
         t.rows = min(256, rows - t.m * 256);
         t.kb = a.kb_all;
         t.k_tail = kBK;
@@ -300,47 +314,47 @@ struct Epilogue {
 
     // Every load is issued, at a place clamped into the tensor where its row or
     // column is out: a branch around each would wait for them in turn.
-    __device__ __forceinline__ void load(int64_t row0, int rows, int col) {
+    __device__ __forceinline__ void load(const Product& p, int64_t row0, int rows, int col) {
         if constexpr (EPI == E_DGATE) {
-            const int c = min(col + 8 * (lane & 3), a.N - 8);
+            const int c = min(col + 8 * (lane & 3), p.N - 8);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = min(8 * i + (lane >> 2), rows - 1);
-                const bf16* p = a.gu + (row0 + r) * a.ld + c;
-                g[i] = __ldcs(reinterpret_cast<const uint4*>(p));
-                u[i] = __ldcs(reinterpret_cast<const uint4*>(p + a.N));
+                const bf16* at = a.gu + (row0 + r) * p.ld + c;
+                g[i] = __ldcs(reinterpret_cast<const uint4*>(at));
+                u[i] = __ldcs(reinterpret_cast<const uint4*>(at + p.N));
             }
         }
     }
 
-    __device__ __forceinline__ void run(uint32_t taddr, int64_t row0, int rows, int col0, int sel) {
+    __device__ __forceinline__ void run(const Product& p, uint32_t taddr, int64_t row0, int rows, int col0) {
         if constexpr (EPI == E_GATE) {
 #pragma unroll 1
-            for (int p = 0; p < 2; ++p) {
-                const int col = col0 + 32 * p, n = (a.N - col) / 8;
-                if (col >= a.N) return;
+            for (int q = 0; q < 2; ++q) {
+                const int col = col0 + 32 * q, n = (p.N - col) / 8;
+                if (col >= p.N) return;
                 float v[32], w[32];
-                tmem_ld32(taddr + static_cast<uint32_t>(32 * p), v);
-                tmem_ld32(taddr + static_cast<uint32_t>(128 + 32 * p), w);
-                uint8_t* gu = reinterpret_cast<uint8_t*>(static_cast<bf16*>(a.out[0]) + row0 * a.ld + col);
+                tmem_ld32(taddr + static_cast<uint32_t>(32 * q), v);
+                tmem_ld32(taddr + static_cast<uint32_t>(128 + 32 * q), w);
+                uint8_t* gu = reinterpret_cast<uint8_t*>(static_cast<bf16*>(p.out) + row0 * p.ld + col);
                 stage_bf16(stg, lane, v);
-                flush(stg, lane, gu, a.ld * 2, rows, n);
+                flush(stg, lane, gu, p.ld * 2, rows, n);
                 stage_bf16(stg, lane, w);
-                flush(stg, lane, gu + static_cast<int64_t>(a.N) * 2, a.ld * 2, rows, n);
+                flush(stg, lane, gu + static_cast<int64_t>(p.N) * 2, p.ld * 2, rows, n);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= sigmoid(v[i]) * w[i];
                 stage_bf16(stg, lane, v);
-                flush(stg, lane, reinterpret_cast<uint8_t*>(a.h + row0 * a.N + col), static_cast<int64_t>(a.N) * 2, rows, n);
+                flush(stg, lane, reinterpret_cast<uint8_t*>(a.h + row0 * p.N + col), static_cast<int64_t>(p.N) * 2, rows, n);
             }
         } else if constexpr (EPI == E_DGATE) {
 #pragma unroll 1
-            for (int p = 0; p < 4; ++p) {
-                const int col = col0 + 32 * p, c = col + 8 * (lane & 3);
-                if (col >= a.N) return;
+            for (int q = 0; q < 4; ++q) {
+                const int col = col0 + 32 * q, c = col + 8 * (lane & 3);
+                if (col >= p.N) return;
                 float acc[4][8];
                 {
                     float v[32];
-                    tmem_ld32(taddr + static_cast<uint32_t>(32 * p), v);
+                    tmem_ld32(taddr + static_cast<uint32_t>(32 * q), v);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // 16 columns at a time; lanes l % 4 = 2 h, 2 h + 1 take them
                         stage_f32(stg, lane, v + 16 * h);
@@ -361,7 +375,7 @@ struct Epilogue {
                 uint4 gn[4], un[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) gn[i] = g[i], un[i] = u[i];
-                if (p < 3 && col + 32 < a.N) load(row0, rows, col + 32);
+                if (q < 3 && col + 32 < p.N) load(p, row0, rows, col + 32);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = 8 * i + (lane >> 2);
@@ -374,44 +388,44 @@ struct Epilogue {
                         dg[x] = acc[i][x] * uv[x] * sg * (1.0f + gv[x] * (1.0f - sg));
                         du[x] = acc[i][x] * gv[x] * sg;
                     }
-                    if (r < rows && c < a.N) {
-                        bf16* dst = static_cast<bf16*>(a.out[0]) + (row0 + r) * a.ld + c;
+                    if (r < rows && c < p.N) {
+                        bf16* dst = static_cast<bf16*>(p.out) + (row0 + r) * p.ld + c;
                         *reinterpret_cast<uint4*>(dst) = pack8(dg);
-                        *reinterpret_cast<uint4*>(dst + a.N) = pack8(du);
+                        *reinterpret_cast<uint4*>(dst + p.N) = pack8(du);
                     }
                 }
             }
         } else {
             const bool as_bf16 = EPI == E_BF16 || (EPI == E_WGRAD && a.out_bf16);
             const int bytes = as_bf16 ? 2 : 4;
-            uint8_t* out = static_cast<uint8_t*>(a.out[sel]) + row0 * a.ld * bytes;
+            uint8_t* out = static_cast<uint8_t*>(p.out) + row0 * p.ld * bytes;
 #pragma unroll 1
-            for (int p = 0; p < 4; ++p) {
-                const int col = col0 + 32 * p;
-                if (col >= a.N) return;
+            for (int q = 0; q < 4; ++q) {
+                const int col = col0 + 32 * q;
+                if (col >= p.N) return;
                 float v[32];
-                tmem_ld32(taddr + static_cast<uint32_t>(32 * p), v);
+                tmem_ld32(taddr + static_cast<uint32_t>(32 * q), v);
                 if (as_bf16) {
                     stage_bf16(stg, lane, v);
-                    flush(stg, lane, out + col * 2, a.ld * 2, rows, (a.N - col) / 8);
+                    flush(stg, lane, out + col * 2, p.ld * 2, rows, (p.N - col) / 8);
                 } else {
                     stage_f32(stg, lane, v);
-                    flush(stg, lane, out + static_cast<int64_t>(col) * 4, a.ld * 4, rows, (a.N - col) / 4);
+                    flush(stg, lane, out + static_cast<int64_t>(col) * 4, p.ld * 4, rows, (p.N - col) / 4);
                     stage_f32(stg, lane, v + 16);
-                    flush(stg, lane, out + static_cast<int64_t>(col) * 4 + 64, a.ld * 4, rows, (a.N - col) / 4 - 4);
+                    flush(stg, lane, out + static_cast<int64_t>(col) * 4 + 64, p.ld * 4, rows, (p.N - col) / 4 - 4);
                 }
             }
         }
     }
 
     // A weight gradient of an expert without rows.
-    __device__ __forceinline__ void zero(int64_t row0, int rows, int col0, int sel) {
+    __device__ __forceinline__ void zero(const Product& p, int64_t row0, int rows, int col0) {
         const int per = a.out_bf16 ? 8 : 4;
         for (int r = 0; r < rows; ++r)
-            for (int c = col0 + per * lane; c < a.N && c < col0 + 128; c += 32 * per) {
-                const int64_t at = (row0 + r) * a.ld + c;
-                uint8_t* p = static_cast<uint8_t*>(a.out[sel]) + at * (a.out_bf16 ? 2 : 4);
-                *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = col0 + per * lane; c < p.N && c < col0 + 128; c += 32 * per) {
+                const int64_t at = (row0 + r) * p.ld + c;
+                uint8_t* dst = static_cast<uint8_t*>(p.out) + at * (a.out_bf16 ? 2 : 4);
+                *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
             }
     }
 };
@@ -464,7 +478,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         mbar_init(never, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < (WG ? a.products : 2); ++i) {
             tma_prefetch_desc(&maps.a[i]);
             tma_prefetch_desc(&maps.b[i]);
         }
@@ -486,12 +500,11 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         off[g] = static_cast<int>(o < 0 ? 0 : (o > a.cap ? a.cap : o));
     }
     __syncthreads();
-    if (warp == 0) {  // a group whose end lies before its start is empty
+    if (!WG && warp == 0) {  // tiles before each group; one whose end lies before its start is empty
         int carry = 0;
         for (int g0 = 0; g0 < a.G; g0 += 32) {
             const int g = g0 + lane;
-            const int rows = g < a.G ? max(0, off[g + 1] - off[g]) : 0;
-            const int n = g < a.G ? (WG ? a.m_tiles : (rows + 255) >> 8) * a.n_tiles : 0;
+            const int n = g < a.G ? ((max(0, off[g + 1] - off[g]) + 255) >> 8) * a.p[0].n_tiles : 0;
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -508,7 +521,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     pair_wait();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const Sched sc{off, start, start[a.G]};
+    const Sched sc{off, start, WG ? a.G * a.group_tiles : start[a.G]};
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const uint32_t peer_abort = peer_addr(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
 
@@ -521,9 +534,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             bool ok = true;
             for (int tile = pair; ok && tile < sc.total; tile += npairs) {
                 const Tile t = decode<WG>(a, sc, tile);
-                const int sel = WG && t.n >= a.n_first ? 1 : 0;
-                const int col0 = (t.n - sel * a.n_first) * SUB * kSubCols;
-                const int subs = min(SUB, (a.N - col0 + kSubCols - 1) / kSubCols);
+                const int col0 = t.n * SUB * kSubCols;
+                const int subs = min(SUB, (a.p[t.j].N - col0 + kSubCols - 1) / kSubCols);
                 const int n0 = col0 + (EPI == E_GATE ? 0 : 128 * static_cast<int>(rank));
                 const uint32_t bytes = static_cast<uint32_t>(1 + subs) * kOperand;
                 for (int kb = 0; kb < t.kb; ++kb) {
@@ -547,12 +559,12 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                     if (WG) {
                         const int y = static_cast<int>(t.row0) + kb * kBK;
                         const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
-                        load_2d(&maps.a[0], sa, bar, m0, y);
-                        load_2d(&maps.a[0], sa + 8192, bar, m0 + 64, y);
+                        load_2d(&maps.a[t.j], sa, bar, m0, y);
+                        load_2d(&maps.a[t.j], sa + 8192, bar, m0 + 64, y);
                         for (int j = 0; j < subs; ++j) {
                             const uint32_t sb = sa + (1 + j) * kOperand;
-                            load_2d(&maps.b[sel], sb, bar, n0 + 256 * j, y);
-                            load_2d(&maps.b[sel], sb + 8192, bar, n0 + 256 * j + 64, y);
+                            load_2d(&maps.b[t.j], sb, bar, n0 + 256 * j, y);
+                            load_2d(&maps.b[t.j], sb + 8192, bar, n0 + 256 * j + 64, y);
                         }
                     } else {
                         const int second = kb >= a.kb_first ? 1 : 0;
@@ -619,8 +631,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         for (int tile = pair; ok && leader && tile < sc.total; tile += npairs) {
             const Tile t = decode<WG>(a, sc, tile);
             if (t.kb == 0) continue;
-            const int col0 = (t.n - (WG && t.n >= a.n_first ? a.n_first : 0)) * SUB * kSubCols;
-            const int subs = SUB == 1 ? 1 : min(SUB, (a.N - col0 + kSubCols - 1) / kSubCols);
+            const int subs = SUB == 1 ? 1 : min(SUB, (a.p[t.j].N - t.n * SUB * kSubCols + kSubCols - 1) / kSubCols);
             int kb = 0;
             const int buf0 = SUB == 1 ? it & 1 : 0;
             const uint32_t use = static_cast<uint32_t>(SUB == 1 ? it >> 1 : it);
@@ -692,8 +703,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             const uint32_t tph = (tail_ph >> st) & 1u;
             tail_ph ^= 1u << st;
             if (!warp_wait(&tail[st], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) break;
-            const int col0 = (t.n - (t.n >= a.n_first ? a.n_first : 0)) * SUB * kSubCols;
-            const int subs = SUB == 1 ? 1 : min(SUB, (a.N - col0 + kSubCols - 1) / kSubCols);
+            const int subs = SUB == 1 ? 1 : min(SUB, (a.p[t.j].N - t.n * SUB * kSubCols + kSubCols - 1) / kSubCols);
             const int from = t.k_tail * 8, to = (t.k_tail + 15) / 16 * 128;  // 16-byte units of a 64-column box
             uint4* box = reinterpret_cast<uint4*>(smem + st * kStageBytes);
             for (int i = from + lane; i < to; i += 32)
@@ -715,21 +725,21 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         for (int tile = pair; ok && tile < sc.total; tile += npairs) {
             const Tile t = decode<WG>(a, sc, tile);
             const int r0 = static_cast<int>(rank) * 128 + q * 32;  // this warp's first row of the tile
-            const int rows = max(0, min(32, (WG ? a.M - t.m * 256 : t.rows) - r0));
-            const int64_t row0 = WG ? static_cast<int64_t>(t.g) * a.M + t.m * 256 + r0 : t.row0 + r0;
-            const int sel = WG && t.n >= a.n_first ? 1 : 0;
-            const int tile_col = (t.n - sel * a.n_first) * SUB * kSubCols;
-            const int subs = SUB == 1 ? 1 : min(SUB, (a.N - tile_col + kSubCols - 1) / kSubCols);
+            const Product& p = a.p[t.j];
+            const int rows = max(0, min(32, (WG ? p.M - t.m * 256 : t.rows) - r0));
+            const int64_t row0 = WG ? static_cast<int64_t>(t.g) * p.M + t.m * 256 + r0 : t.row0 + r0;
+            const int tile_col = t.n * SUB * kSubCols;
+            const int subs = SUB == 1 ? 1 : min(SUB, (p.N - tile_col + kSubCols - 1) / kSubCols);
             for (int j = 0; j < subs; ++j) {
                 const int col0 = tile_col + j * kSubCols + half * (kSubCols / 2);
                 if (WG && t.kb == 0) {
-                    epi.zero(row0, rows, col0, sel);
+                    epi.zero(p, row0, rows, col0);
                     continue;
                 }
                 const int buf = SUB == 1 ? it & 1 : j;
                 const uint32_t use = SUB == 1 ? static_cast<uint32_t>(it >> 1) : (j ? uses1 : static_cast<uint32_t>(it));
-                const bool mine = rows > 0 && col0 < a.N;
-                if (mine) epi.load(row0, rows, col0);
+                const bool mine = rows > 0 && col0 < p.N;
+                if (mine) epi.load(p, row0, rows, col0);
                 if (!warp_wait(a.never_ready ? never : &tfull[buf], a.never_ready ? 0u : use & 1u, a, DEV_TIMEOUT_EPI_TFULL, abort_flag,
                                peer_abort)) {
                     ok = false;
@@ -738,7 +748,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 tc_fence_after();
                 const uint32_t taddr = tmem_base + static_cast<uint32_t>(buf) * 256u + (static_cast<uint32_t>(q * 32) << 16) +
                                        static_cast<uint32_t>(half * (kSubCols / 2));
-                if (mine) epi.run(taddr, row0, rows, col0, sel);
+                if (mine) epi.run(p, taddr, row0, rows, col0);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(leader_tempty + 8u * buf);
@@ -858,19 +868,41 @@ int launch_sub(const Maps& maps, Args a, int64_t max_tiles, cudaStream_t st) {
 constexpr int wide_from(int epi) { return epi == E_DGATE ? 128 : (epi == E_GATE ? 64 : 32); }
 
 // `kb`: k-blocks of a tile (of an average one, for weight gradients); `row_tiles`:
-// an upper bound of the row tiles of all groups; `outs`: outputs side by side.
+// token-major: an upper bound of all groups' row tiles.
 template <int EPI, bool B_MN>
-int launch(const Maps& maps, Args a, int kb, int64_t row_tiles, int outs, cudaStream_t st) {
+int launch(const Maps& maps, Args a, int kb, int64_t row_tiles, cudaStream_t st) {
     if (a.G < 1 || a.G > kMaxGroups) return -2;
     const WaitSettings wt = wait_settings();
     a.wait_limit = wt.wait_limit ? wt.wait_limit : kWaitLimit;
     a.never_ready = wt.dep_never_ready;
     const int sub_cols = EPI == E_GATE ? 128 : 256;
-    const int sub = kb >= wide_from(EPI) && a.N > sub_cols ? 2 : 1;
-    a.n_first = ceil_div(a.N, sub * sub_cols);
-    a.n_tiles = outs * a.n_first;
-    return sub == 2 ? launch_sub<EPI, B_MN, 2>(maps, a, row_tiles * a.n_tiles, st)
-                    : launch_sub<EPI, B_MN, 1>(maps, a, row_tiles * a.n_tiles, st);
+    int widest = 0;
+    for (int j = 0; j < a.products; ++j) widest = a.p[j].N > widest ? a.p[j].N : widest;
+    const int sub = kb >= wide_from(EPI) && widest > sub_cols ? 2 : 1;
+    for (int j = 0; j < a.products; ++j) {
+        Product& p = a.p[j];
+        p.n_tiles = ceil_div(p.N, sub * sub_cols);
+        p.m_tiles = ceil_div(p.M, 256);
+        a.group_tiles += p.m_tiles * p.n_tiles;
+    }
+    const int64_t tiles = EPI == E_WGRAD ? static_cast<int64_t>(a.G) * a.group_tiles : row_tiles * a.p[0].n_tiles;
+    return sub == 2 ? launch_sub<EPI, B_MN, 2>(maps, a, tiles, st) : launch_sub<EPI, B_MN, 1>(maps, a, tiles, st);
+}
+
+// What the token-major products share.
+Args token_major(const int32_t* off, int64_t rows, int E, int N, int64_t ld, void* out, int kb_first, int kb_all, int* status) {
+    Args a{};
+    a.off = off;
+    a.cap = rows;
+    a.G = E;
+    a.kb_first = kb_first;
+    a.kb_all = kb_all;
+    a.products = 1;
+    a.p[0].N = N;
+    a.p[0].ld = ld;
+    a.p[0].out = out;
+    a.status = status;
+    return a;
 }
 
 // Upper bound of a token-major launch's row tiles: a group's last one may be partial.
@@ -886,17 +918,9 @@ int launch_train_gate(const bf16* x, const int32_t* off, int64_t rows, int E, in
         !map_weights(&m.b[1], W3, E, d, f, 64))
         return -3;
     m.a[1] = m.a[0];
-    Args a{};
-    a.off = off;
-    a.cap = rows;
-    a.G = E;
-    a.N = f;
-    a.kb_first = a.kb_all = ceil_div(d, kBK);
-    a.ld = 2 * static_cast<int64_t>(f);
-    a.out[0] = gu;
+    Args a = token_major(off, rows, E, f, 2 * static_cast<int64_t>(f), gu, ceil_div(d, kBK), ceil_div(d, kBK), status);
     a.h = h;
-    a.status = status;
-    return launch<E_GATE, true>(m, a, a.kb_all, row_tile_bound(rows, E), 1, st);
+    return launch<E_GATE, true>(m, a, a.kb_all, row_tile_bound(rows, E), st);
 }
 
 int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2, float* y,
@@ -906,16 +930,8 @@ int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, in
     if (!map_matrix(&m.a[0], h, rows, f, f, 128) || !map_weights(&m.b[0], W2, E, f, d, 64)) return -3;
     m.a[1] = m.a[0];
     m.b[1] = m.b[0];
-    Args a{};
-    a.off = off;
-    a.cap = rows;
-    a.G = E;
-    a.N = d;
-    a.kb_first = a.kb_all = ceil_div(f, kBK);
-    a.ld = d;
-    a.out[0] = y;
-    a.status = status;
-    return launch<E_F32, true>(m, a, a.kb_all, row_tile_bound(rows, E), 1, st);
+    Args a = token_major(off, rows, E, d, d, y, ceil_div(f, kBK), ceil_div(f, kBK), status);
+    return launch<E_F32, true>(m, a, a.kb_all, row_tile_bound(rows, E), st);
 }
 
 int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2,
@@ -925,17 +941,9 @@ int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, 
     if (!map_matrix(&m.a[0], dy, rows, d, d, 128) || !map_weights(&m.b[0], W2, E, f, d, 128)) return -3;
     m.a[1] = m.a[0];
     m.b[1] = m.b[0];
-    Args a{};
-    a.off = off;
-    a.cap = rows;
-    a.G = E;
-    a.N = f;
-    a.kb_first = a.kb_all = ceil_div(d, kBK);
-    a.ld = 2 * static_cast<int64_t>(f);
-    a.out[0] = dgu;
+    Args a = token_major(off, rows, E, f, 2 * static_cast<int64_t>(f), dgu, ceil_div(d, kBK), ceil_div(d, kBK), status);
     a.gu = gu;
-    a.status = status;
-    return launch<E_DGATE, false>(m, a, a.kb_all, row_tile_bound(rows, E), 1, st);
+    return launch<E_DGATE, false>(m, a, a.kb_all, row_tile_bound(rows, E), st);
 }
 
 int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W1,
@@ -946,44 +954,32 @@ int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, in
     if (!map_matrix(&m.a[0], dgu, rows, f, ld, 128) || !map_matrix(&m.a[1], dgu + f, rows, f, ld, 128) ||
         !map_weights(&m.b[0], W1, E, d, f, 128) || !map_weights(&m.b[1], W3, E, d, f, 128))
         return -3;
-    Args a{};
-    a.off = off;
-    a.cap = rows;
-    a.G = E;
-    a.N = d;
-    a.kb_first = ceil_div(f, kBK);
-    a.kb_all = 2 * a.kb_first;
-    a.ld = d;
-    a.out[0] = dx;
-    a.status = status;
-    return launch<E_BF16, false>(m, a, a.kb_all, row_tile_bound(rows, E), 1, st);
+    Args a = token_major(off, rows, E, d, d, dx, ceil_div(f, kBK), 2 * ceil_div(f, kBK), status);
+    return launch<E_BF16, false>(m, a, a.kb_all, row_tile_bound(rows, E), st);
 }
 
-int launch_train_dw(const bf16* left, int m_cols, const bf16* right0, const bf16* right1, int64_t right_ld, int n_cols,
-                    const int32_t* off, int64_t chunk, int64_t rows, int G, void* out0, void* out1, int64_t out_ld,
-                    bool out_bf16, int* status, cudaStream_t st) {
+int launch_train_dw(const WeightGradient* w, int n, const int32_t* off, int64_t chunk, int64_t rows, int G, bool out_bf16,
+                    int* status, cudaStream_t st) {
+    if (n < 1 || n > kProducts) return -2;
     Maps m;
     std::memset(&m, 0, sizeof(m));
-    if (!map_matrix(&m.a[0], left, rows, m_cols, m_cols, 64) || !map_matrix(&m.b[0], right0, rows, n_cols, right_ld, 64))
-        return -3;
-    m.a[1] = m.a[0];
-    m.b[1] = m.b[0];
-    if (right1 && !map_matrix(&m.b[1], right1, rows, n_cols, right_ld, 64)) return -3;
     Args a{};
+    for (int j = 0; j < n; ++j) {
+        if (!map_matrix(&m.a[j], w[j].left, rows, w[j].M, w[j].M, 64) || !map_matrix(&m.b[j], w[j].right, rows, w[j].N, w[j].right_ld, 64))
+            return -3;
+        a.p[j].M = w[j].M;
+        a.p[j].N = w[j].N;
+        a.p[j].ld = w[j].N;
+        a.p[j].out = w[j].out;
+    }
+    a.products = n;
     a.off = off;
     a.chunk = chunk;
     a.cap = rows;
     a.G = G;
-    a.M = m_cols;
-    a.N = n_cols;
-    a.m_tiles = ceil_div(m_cols, 256);
-    a.ld = out_ld;
-    a.out[0] = out0;
-    a.out[1] = out1;
     a.out_bf16 = out_bf16 ? 1 : 0;
     a.status = status;
-    const int kb = ceil_div(off ? rows / G : chunk, kBK);
-    return launch<E_WGRAD, true>(m, a, kb, static_cast<int64_t>(G) * a.m_tiles, right1 ? 2 : 1, st);
+    return launch<E_WGRAD, true>(m, a, ceil_div(off ? rows / G : chunk, kBK), 0, st);
 }
 
 }  // namespace moe
