@@ -61,7 +61,9 @@ namespace {
 constexpr int kBK = 64;
 constexpr uint32_t kOperand = 16384u;  // one CTA's half of an operand: 128 x 64 bf16
 constexpr uint32_t kRingBytes = 12 * kOperand;
-constexpr int kStaging = 2048;  // per epilogue warp
+// Output staging of an epilogue warp.  (Weight gradients need no table of first
+// tiles, so 4 KB fit beside the ring.)
+constexpr int staging_of(bool wgrad) { return wgrad ? 4096 : 2048; }
 constexpr uint32_t kTmemCols = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;   // weight gradients: one more warp, which clears tails
@@ -101,6 +103,7 @@ struct Args {
 struct Maps {
     CUtensorMap a[kProducts];
     CUtensorMap b[kProducts];
+    CUtensorMap c[kProducts];  // weight gradients: the outputs [G, M, N], boxes of 128 bytes x 32 rows
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -300,6 +303,64 @@ __device__ __forceinline__ void stage_f32(uint8_t* stg, int lane, const float* v
         *reinterpret_cast<float4*>(chunk_at(stg, lane, j)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
+// A weight gradient's accumulators go to registers at once, which frees them
+// for the next tile, and leave as TMA stores of 32 rows x 128 bytes: a tile of
+// few k-blocks is bound by this epilogue (64 experts of 9 rows, 5856 x 400:
+// 367 us with the stores above, 303 so).  The store clips at M and N.
+template <int EPI>
+struct WeightStore {
+    uint32_t acc[4][32];
+    __device__ __forceinline__ void fetch(uint32_t taddr) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                : "=r"(acc[q][0]),"=r"(acc[q][1]),"=r"(acc[q][2]),"=r"(acc[q][3]),"=r"(acc[q][4]),"=r"(acc[q][5]),"=r"(acc[q][6]),"=r"(acc[q][7]),"=r"(acc[q][8]),"=r"(acc[q][9]),"=r"(acc[q][10]),"=r"(acc[q][11]),"=r"(acc[q][12]),"=r"(acc[q][13]),"=r"(acc[q][14]),"=r"(acc[q][15]),"=r"(acc[q][16]),"=r"(acc[q][17]),"=r"(acc[q][18]),"=r"(acc[q][19]),"=r"(acc[q][20]),"=r"(acc[q][21]),"=r"(acc[q][22]),"=r"(acc[q][23]),"=r"(acc[q][24]),"=r"(acc[q][25]),"=r"(acc[q][26]),"=r"(acc[q][27]),"=r"(acc[q][28]),"=r"(acc[q][29]),"=r"(acc[q][30]),"=r"(acc[q][31])
+                : "r"(taddr + 32u * q));
+#pragma unroll
+        for (int q = 0; q < 4; ++q)  // nothing that uses them can move ahead of the wait
+            asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(acc[q][0]),"+r"(acc[q][1]),"+r"(acc[q][2]),"+r"(acc[q][3]),"+r"(acc[q][4]),"+r"(acc[q][5]),"+r"(acc[q][6]),"+r"(acc[q][7]),"+r"(acc[q][8]),"+r"(acc[q][9]),"+r"(acc[q][10]),"+r"(acc[q][11]),"+r"(acc[q][12]),"+r"(acc[q][13]),"+r"(acc[q][14]),"+r"(acc[q][15]),"+r"(acc[q][16]),"+r"(acc[q][17]),"+r"(acc[q][18]),"+r"(acc[q][19]),"+r"(acc[q][20]),"+r"(acc[q][21]),"+r"(acc[q][22]),"+r"(acc[q][23]),"+r"(acc[q][24]),"+r"(acc[q][25]),"+r"(acc[q][26]),"+r"(acc[q][27]),"+r"(acc[q][28]),"+r"(acc[q][29]),"+r"(acc[q][30]),"+r"(acc[q][31]));
+    }
+    // To columns col0 .. col0 + 127 of rows row .. row + 31 of matrix g.
+    __device__ __forceinline__ void store(const CUtensorMap* map, uint8_t* stg, int lane, bool as_bf16, int N, int col0, int row, int g) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int col = col0 + 32 * (as_bf16 ? q & ~1 : q);
+            if (col >= N) return;
+            if (!as_bf16 || !(q & 1)) {  // the box that was last stored from here has been read
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+            }
+            uint8_t* row_at = stg + lane * 128;
+            if (as_bf16) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(acc[q][8 * j + i]);
+                    *reinterpret_cast<uint4*>(row_at + (((4 * (q & 1) + j) ^ (lane & 7)) << 4)) = pack8(v);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4*>(row_at + ((j ^ (lane & 7)) << 4)) =
+                        make_uint4(acc[q][4 * j], acc[q][4 * j + 1], acc[q][4 * j + 2], acc[q][4 * j + 3]);
+            }
+            if (!as_bf16 || (q & 1)) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+                                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(stg)), "r"(col), "r"(row), "r"(g) : "memory");
+                    bulk_commit();
+                }
+            }
+        }
+    }
+};
+
 // A warp's part of a 256-column sub-tile: 32 rows (`rows` of them valid) from
 // output row `row0`, columns from `col0` up to the width N: 128 of them, 64 of
 // each projection for E_GATE.  `taddr` is its first accumulator column.
@@ -396,7 +457,7 @@ struct Epilogue {
                 }
             }
         } else {
-            const bool as_bf16 = EPI == E_BF16 || (EPI == E_WGRAD && a.out_bf16);
+            const bool as_bf16 = EPI == E_BF16;
             const int bytes = as_bf16 ? 2 : 4;
             uint8_t* out = static_cast<uint8_t*>(p.out) + row0 * p.ld * bytes;
 #pragma unroll 1
@@ -446,7 +507,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     constexpr int kSubCols = EPI == E_GATE ? 128 : 256;  // output columns of a sub-tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes + kEpiWarps * kStaging);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes + kEpiWarps * staging_of(WG));
     uint64_t* empty = full + kStages;
     uint64_t* tail = empty + kStages;
     uint64_t* clear = tail + kStages;
@@ -458,7 +519,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     uint32_t* issued = tmem_slot + 2;  // [rank][stage uses issued, stages whose last use was a tail], [rank][use_bytes]
     int* off = reinterpret_cast<int*>(issued + 4 + 2 * kMaxStages);
-    int* start = off + kMaxGroups + 1;
+    int* start = off + kMaxGroups + 1;  // token-major only
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
@@ -718,7 +779,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         // a quarter take the two column halves.
         const int q = warp & 3, half = (warp - 2) >> 2;
         const uint32_t leader_tempty = peer_addr(smem_u32(tempty), 0);
-        Epilogue<EPI> epi{a, smem + kRingBytes + (warp - 2) * kStaging, lane};
+        uint8_t* const stg = smem + kRingBytes + (warp - 2) * staging_of(WG);
+        Epilogue<EPI> epi{a, stg, lane};
         int it = 0;
         uint32_t uses1 = 0;
         bool ok = true;
@@ -739,7 +801,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 const int buf = SUB == 1 ? it & 1 : j;
                 const uint32_t use = SUB == 1 ? static_cast<uint32_t>(it >> 1) : (j ? uses1 : static_cast<uint32_t>(it));
                 const bool mine = rows > 0 && col0 < p.N;
-                if (mine) epi.load(p, row0, rows, col0);
+                if (mine && !WG) epi.load(p, row0, rows, col0);
                 if (!warp_wait(a.never_ready ? never : &tfull[buf], a.never_ready ? 0u : use & 1u, a, DEV_TIMEOUT_EPI_TFULL, abort_flag,
                                peer_abort)) {
                     ok = false;
@@ -748,16 +810,26 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 tc_fence_after();
                 const uint32_t taddr = tmem_base + static_cast<uint32_t>(buf) * 256u + (static_cast<uint32_t>(q * 32) << 16) +
                                        static_cast<uint32_t>(half * (kSubCols / 2));
-                if (mine) epi.run(p, taddr, row0, rows, col0);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_cluster(leader_tempty + 8u * buf);
+                if constexpr (WG) {
+                    WeightStore<EPI> w;
+                    w.fetch(taddr);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(leader_tempty + 8u * buf);
+                    if (mine) w.store(&maps.c[t.j], stg, lane, a.out_bf16, p.N, col0, t.m * 256 + r0, t.g);
+                } else {
+                    if (mine) epi.run(p, taddr, row0, rows, col0);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(leader_tempty + 8u * buf);
+                }
             }
             if (!(WG && t.kb == 0)) {
                 ++it;
                 uses1 += subs == 2 ? 1u : 0u;
             }
         }
+        if (WG && lane == 0) bulk_wait_all();
     }
 
     // No copy is in flight when the pair ends.  A complete run issued the same
@@ -831,15 +903,32 @@ bool map_weights(CUtensorMap* m, const bf16* base, int64_t mats, int64_t rows, i
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Output matrices [mats, rows, cols], boxes of 128 bytes x 32 rows of one matrix.
+bool map_output(CUtensorMap* m, void* base, bool as_bf16, int64_t mats, int64_t rows, int64_t cols) {
+    auto enc = map_encoder();
+    if (!enc) return false;
+    const cuuint64_t size = as_bf16 ? 2 : 4;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(mats)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * size, static_cast<cuuint64_t>(rows) * cols * size};
+    cuuint32_t box[3] = {as_bf16 ? 64u : 32u, 32u, 1u}, es[3] = {1, 1, 1};
+    return enc(m, as_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-constexpr size_t kSmem = 1024 + kRingBytes + kEpiWarps * kStaging + (4 * kMaxStages + 6) * 8 + 8 +
-                         (4 + 2 * kMaxStages) * 4 + 2 * (kMaxGroups + 1) * 4;
+constexpr size_t smem_of(bool wgrad) {
+    return 1024 + kRingBytes + kEpiWarps * staging_of(wgrad) + (4 * kMaxStages + 6) * 8 + 8 + (4 + 2 * kMaxStages) * 4 +
+           (wgrad ? 1 : 2) * (kMaxGroups + 1) * 4;
+}
+static_assert(smem_of(true) <= 232448 && smem_of(false) <= 232448, "227 KB a CTA");
 
 template <int EPI, bool B_MN, int SUB>
 int launch_sub(const Maps& maps, Args a, int64_t max_tiles, cudaStream_t st) {
     static std::atomic<unsigned long long> attr_done{0};
     const auto kernel = train_gemm_kernel<EPI, B_MN, SUB>;
+    constexpr size_t kSmem = smem_of(EPI == E_WGRAD);
     if (smem_attr_once(reinterpret_cast<const void*>(kernel), static_cast<int>(kSmem), attr_done) != 0) return -3;
     int pairs = num_sms() / 2;
     if (pairs < 1) return -3;
@@ -965,7 +1054,8 @@ int launch_train_dw(const WeightGradient* w, int n, const int32_t* off, int64_t 
     std::memset(&m, 0, sizeof(m));
     Args a{};
     for (int j = 0; j < n; ++j) {
-        if (!map_matrix(&m.a[j], w[j].left, rows, w[j].M, w[j].M, 64) || !map_matrix(&m.b[j], w[j].right, rows, w[j].N, w[j].right_ld, 64))
+        if (!map_matrix(&m.a[j], w[j].left, rows, w[j].M, w[j].M, 64) || !map_matrix(&m.b[j], w[j].right, rows, w[j].N, w[j].right_ld, 64) ||
+            !map_output(&m.c[j], w[j].out, out_bf16, G, w[j].M, w[j].N))
             return -3;
         a.p[j].M = w[j].M;
         a.p[j].N = w[j].N;
