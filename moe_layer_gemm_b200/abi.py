@@ -425,74 +425,71 @@ def moe_expert_ffn_slots(dims, x_perm, offsets, expert_slot, n_slots: int, W13c,
 
 # ---------------------------------------------------------------- training
 
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+# These calls check more than the ones above: device, type, contiguity and
+# size of every tensor, since a training program hands over a dozen at a time.
+# The checks that pass take one short expression a tensor.
 
-
-class _On:
-    """Checks one call's tensors and launches it on their device and its current stream."""
-
-    __slots__ = ("index", "stream")
-
-    def __init__(self, anchor, stream):
-        if not isinstance(anchor, torch.Tensor) or not anchor.is_cuda:
-            raise ValueError("expected CUDA tensors")
-        self.index, self.stream = anchor.get_device(), stream
-
-    def ptr(self, t, numel: int, name: str, dtype=None, optional: bool = False):
-        """Address of a contiguous tensor of at least `numel` values on the call's device."""
-        if t is None:
-            if optional:
-                return None
-            raise ValueError(f"{name}: required")
-        if type(t) is torch.Tensor and t.dtype == (dtype or t.dtype) and t.get_device() == self.index and t.numel() >= numel and t.is_contiguous():
+def _need(t, n: int, dtype, dev: int, name: str):
+    """Address of a contiguous tensor of at least `n` values of `dtype` on CUDA device `dev`."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
             return t.data_ptr()
-        p = _ptr(t, dtype, name)
-        if t.get_device() != self.index:
-            raise ValueError(f"{name}: on {t.device}, the call's other tensors are on cuda:{self.index}")
-        if t.numel() < numel:
-            raise ValueError(f"{name}: {t.numel()} values, {numel} needed")
-        return p
-
-    def either(self, t, numel: int, name: str, like=None, optional: bool = False):
-        """Address and is_bf16 flag of a bf16 or fp32 tensor (of `like`'s type, where given)."""
-        if t is None and optional:
-            return None, 0
-        if isinstance(t, torch.Tensor) and t.dtype not in (BF16, F32):
-            raise TypeError(f"{name}: expected {BF16} or {F32}, got {t.dtype}")
-        return self.ptr(t, numel, name, None if like is None else like.dtype, optional), int(t is not None and t.dtype == BF16)
-
-    def call(self, name: str, *args):
-        fn = getattr(_lib or load(), name)
-        if torch.cuda.current_device() == self.index:
-            status = fn(*args, self._stream())
-        else:
-            with torch.cuda.device(self.index):
-                status = fn(*args, self._stream())
-        if status != MOE_OK:
-            _check(name, status)
-
-    def _stream(self):
-        if self.stream is not None:
-            return _stream(self.stream)
-        return _raw_stream(self.index) if _raw_stream is not None else torch.cuda.current_stream(self.index).cuda_stream
+    except AttributeError:
+        pass
+    if t is None:
+        raise ValueError(f"{name}: required")
+    _ptr(t, dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the call's other tensors are on cuda:{dev}")
+    raise ValueError(f"{name}: {t.numel()} values, {n} needed")
 
 
-def _rows_of(x, name):
+def _may(t, n: int, dtype, dev: int, name: str):
+    """The same, or None."""
+    return None if t is None else _need(t, n, dtype, dev, name)
+
+
+def _float_type(t, name: str):
+    """Type of a bf16 or fp32 tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype is not BF16 and t.dtype is not F32:
+        raise TypeError(f"{name}: expected {BF16} or {F32}, got {t.dtype}")
+    return t.dtype
+
+
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return t.get_device()
+
+
+def _launch(fn, name: str, dev: int, stream, args):
+    """Run a library call on device `dev` and, unless told otherwise, its current stream."""
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _launch(fn, name, dev, stream, args)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    status = fn(*args, st)
+    if status != MOE_OK:
+        _check(name, status)
+
+
+def _rows_of(x):
     if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.shape[-1] == 0:
-        raise ValueError(f"{name}: expected a tensor [..., d_model]")
-    return x.numel() // x.shape[-1], int(x.shape[-1])
+        raise ValueError("x: expected a tensor [..., d_model]")
+    d = x.shape[-1]
+    return x.numel() // d, d
 
 
 def moe_layernorm(x, gamma, beta, eps: float, y, mean=None, rstd=None, stream=None):
     """Layer norm over x's last axis (x, y bf16 or fp32; gamma, beta both bf16 or both fp32, or None)."""
-    on = _On(x, stream)
-    T, d = _rows_of(x, "x")
-    xp, xb = on.either(x, T * d, "x")
+    (T, d), dev, xt = _rows_of(x), _device_of(x, "x"), _float_type(x, "x")
     w = gamma if gamma is not None else beta
-    gp, gb = on.either(gamma, d, "gamma", w, True)
-    bp, bb = on.either(beta, d, "beta", w, True)
-    on.call("moe_layernorm", T, d, xp, xb, gp, bp, gb | bb, eps, on.ptr(y, T * d, "y", x.dtype),
-            on.ptr(mean, T, "mean", F32, True), on.ptr(rstd, T, "rstd", F32, True))
+    wt = F32 if w is None else _float_type(w, "gamma" if w is gamma else "beta")
+    _launch((_lib or load()).moe_layernorm, "moe_layernorm", dev, stream, (
+        T, d, _need(x, T * d, xt, dev, "x"), xt is BF16, _may(gamma, d, wt, dev, "gamma"), _may(beta, d, wt, dev, "beta"),
+        wt is BF16, eps, _need(y, T * d, xt, dev, "y"), _may(mean, T, F32, dev, "mean"), _may(rstd, T, F32, dev, "rstd")))
 
 
 def moe_layernorm_workspace_size(T: int, d_model: int) -> int:
@@ -503,60 +500,61 @@ def moe_layernorm_workspace_size(T: int, d_model: int) -> int:
 
 def moe_layernorm_backward(dy, x, gamma, mean, rstd, dx_add, dx, dgamma, dbeta, ws, stream=None):
     """Gradients of moe_layernorm; dx_add is added to dx (see the header)."""
-    on = _On(x, stream)
-    T, d = _rows_of(x, "x")
-    xp, xb = on.either(x, T * d, "x")
-    w = next((t for t in (gamma, dgamma, dbeta) if t is not None), None)
-    gp, gb = on.either(gamma, d, "gamma", w, True)
-    dgp, dgb = on.either(dgamma, d, "dgamma", w, True)
-    dbp, dbb = on.either(dbeta, d, "dbeta", w, True)
-    on.call("moe_layernorm_backward", T, d, on.ptr(dy, T * d, "dy", x.dtype), xp, xb, gp, gb | dgb | dbb,
-            on.ptr(mean, T, "mean", F32), on.ptr(rstd, T, "rstd", F32), on.ptr(dx_add, T * d, "dx_add", x.dtype, True),
-            on.ptr(dx, T * d, "dx", x.dtype, True), dgp, dbp, on.ptr(ws, 0, "ws", torch.uint8, True),
-            0 if ws is None else ws.numel())
+    (T, d), dev, xt = _rows_of(x), _device_of(x, "x"), _float_type(x, "x")
+    n = T * d
+    w = gamma if gamma is not None else dgamma if dgamma is not None else dbeta
+    wt = F32 if w is None else _float_type(w, "gamma, dgamma or dbeta")
+    _launch((_lib or load()).moe_layernorm_backward, "moe_layernorm_backward", dev, stream, (
+        T, d, _need(dy, n, xt, dev, "dy"), _need(x, n, xt, dev, "x"), xt is BF16, _may(gamma, d, wt, dev, "gamma"), wt is BF16,
+        _need(mean, T, F32, dev, "mean"), _need(rstd, T, F32, dev, "rstd"), _may(dx_add, n, xt, dev, "dx_add"),
+        _may(dx, n, xt, dev, "dx"), _may(dgamma, d, wt, dev, "dgamma"), _may(dbeta, d, wt, dev, "dbeta"),
+        _may(ws, 0, torch.uint8, dev, "ws"), 0 if ws is None else ws.numel()))
 
 
 def moe_ffn_train(dims, x_perm, offsets, W1, W3, W2, gu, h, y_perm, ws, stream=None):
     """The experts' gated FFN from unpacked weights, keeping gu and h for moe_ffn_backward."""
-    on, c = _On(x_perm, stream), _dims(dims)
+    c, dev = _dims(dims), _device_of(x_perm, "x_perm")
     A, d, f, E = c.T * c.K, c.d_model, c.d_ff, c.E
-    on.call("moe_ffn_train", ctypes.byref(c), on.ptr(x_perm, A * d, "x_perm", BF16), on.ptr(offsets, E + 1, "offsets", I32),
-            on.ptr(W1, E * d * f, "W1", BF16), on.ptr(W3, E * d * f, "W3", BF16), on.ptr(W2, E * f * d, "W2", BF16),
-            on.ptr(gu, A * 2 * f, "gu", BF16), on.ptr(h, A * f, "h", BF16), on.ptr(y_perm, A * d, "y_perm", F32),
-            on.ptr(ws, 0, "ws", torch.uint8), ws.numel())
+    n = E * d * f
+    _launch((_lib or load()).moe_ffn_train, "moe_ffn_train", dev, stream, (
+        ctypes.byref(c), _need(x_perm, A * d, BF16, dev, "x_perm"), _need(offsets, E + 1, I32, dev, "offsets"),
+        _need(W1, n, BF16, dev, "W1"), _need(W3, n, BF16, dev, "W3"), _need(W2, n, BF16, dev, "W2"),
+        _need(gu, 2 * A * f, BF16, dev, "gu"), _need(h, A * f, BF16, dev, "h"), _need(y_perm, A * d, F32, dev, "y_perm"),
+        _need(ws, 0, torch.uint8, dev, "ws"), ws.numel()))
 
 
 def moe_ffn_backward(dims, dy_perm, x_perm, offsets, W1, W3, W2, gu, h, dgu, dx_perm, dW1, dW3, dW2, ws, stream=None):
     """Gradients of moe_ffn_train (dW1, dW3, dW2 all bf16 or all fp32; None: not wanted)."""
-    on, c = _On(dy_perm, stream), _dims(dims)
+    c, dev = _dims(dims), _device_of(dy_perm, "dy_perm")
     A, d, f, E = c.T * c.K, c.d_model, c.d_ff, c.E
-    like = dW1 if dW1 is not None else dW2
-    p1, b1 = on.either(dW1, E * d * f, "dW1", like, True)
-    p3, b3 = on.either(dW3, E * d * f, "dW3", like, True)
-    p2, b2 = on.either(dW2, E * f * d, "dW2", like, True)
-    on.call("moe_ffn_backward", ctypes.byref(c), on.ptr(dy_perm, A * d, "dy_perm", BF16),
-            on.ptr(x_perm, A * d, "x_perm", BF16, True), on.ptr(offsets, E + 1, "offsets", I32),
-            on.ptr(W1, E * d * f, "W1", BF16, True), on.ptr(W3, E * d * f, "W3", BF16, True), on.ptr(W2, E * f * d, "W2", BF16),
-            on.ptr(gu, A * 2 * f, "gu", BF16), on.ptr(h, A * f, "h", BF16, True), on.ptr(dgu, A * 2 * f, "dgu", BF16),
-            on.ptr(dx_perm, A * d, "dx_perm", BF16, True), p1, p3, p2, b1 | b3 | b2, on.ptr(ws, 0, "ws", torch.uint8), ws.numel())
+    n = E * d * f
+    w = dW1 if dW1 is not None else dW2
+    wt = BF16 if w is None else _float_type(w, "dW1 or dW2")
+    _launch((_lib or load()).moe_ffn_backward, "moe_ffn_backward", dev, stream, (
+        ctypes.byref(c), _need(dy_perm, A * d, BF16, dev, "dy_perm"), _may(x_perm, A * d, BF16, dev, "x_perm"),
+        _need(offsets, E + 1, I32, dev, "offsets"), _may(W1, n, BF16, dev, "W1"), _may(W3, n, BF16, dev, "W3"),
+        _need(W2, n, BF16, dev, "W2"), _need(gu, 2 * A * f, BF16, dev, "gu"), _may(h, A * f, BF16, dev, "h"),
+        _need(dgu, 2 * A * f, BF16, dev, "dgu"), _may(dx_perm, A * d, BF16, dev, "dx_perm"), _may(dW1, n, wt, dev, "dW1"),
+        _may(dW3, n, wt, dev, "dW3"), _may(dW2, n, wt, dev, "dW2"), wt is BF16, _need(ws, 0, torch.uint8, dev, "ws"), ws.numel()))
 
 
 def moe_combine_backward(dims, dy, y_perm, inv, topk_w, dy_perm, dtopk_w=None, stream=None):
     """Gradients of moe_combine (dy bf16 or fp32; y_perm is read only for dtopk_w)."""
-    on, c = _On(dy, stream), _dims(dims)
+    c, dev, dt = _dims(dims), _device_of(dy, "dy"), _float_type(dy, "dy")
     T, A, d = c.T, c.T * c.K, c.d_model
-    dyp, db = on.either(dy, T * d, "dy")
-    on.call("moe_combine_backward", ctypes.byref(c), dyp, db, on.ptr(y_perm, A * d, "y_perm", F32, dtopk_w is None),
-            on.ptr(inv, A, "inv", I32), on.ptr(topk_w, A, "topk_w", F32), on.ptr(dy_perm, A * d, "dy_perm", BF16),
-            on.ptr(dtopk_w, A, "dtopk_w", F32, True))
+    _launch((_lib or load()).moe_combine_backward, "moe_combine_backward", dev, stream, (
+        ctypes.byref(c), _need(dy, T * d, dt, dev, "dy"), dt is BF16,
+        (_may if dtopk_w is None else _need)(y_perm, A * d, F32, dev, "y_perm"), _need(inv, A, I32, dev, "inv"),
+        _need(topk_w, A, F32, dev, "topk_w"), _need(dy_perm, A * d, BF16, dev, "dy_perm"), _may(dtopk_w, A, F32, dev, "dtopk_w")))
 
 
 def moe_permute_backward(dims, dx_perm, inv, dx, stream=None):
     """Rows' gradients summed back to their tokens (dx bf16 or fp32)."""
-    on, c = _On(dx_perm, stream), _dims(dims)
+    c, dev, xt = _dims(dims), _device_of(dx_perm, "dx_perm"), _float_type(dx, "dx")
     A, d = c.T * c.K, c.d_model
-    dxp, db = on.either(dx, c.T * d, "dx")
-    on.call("moe_permute_backward", ctypes.byref(c), on.ptr(dx_perm, A * d, "dx_perm", BF16), on.ptr(inv, A, "inv", I32), dxp, db)
+    _launch((_lib or load()).moe_permute_backward, "moe_permute_backward", dev, stream, (
+        ctypes.byref(c), _need(dx_perm, A * d, BF16, dev, "dx_perm"), _need(inv, A, I32, dev, "inv"),
+        _need(dx, c.T * d, xt, dev, "dx"), xt is BF16))
 
 
 def moe_route_backward_workspace_size(dims) -> int:
@@ -569,16 +567,16 @@ def moe_route_backward_workspace_size(dims) -> int:
 def moe_route_backward(dims, x, Wr, logits, topk_idx, topk_w, dtopk_w, counts, aux_coef: float, z_coef: float, dx_perm, inv,
                        dx, dWr, dlogits, ws, stream=None):
     """Gradients of moe_route, with the dispatch's gradient added into dx where dx_perm and inv are given."""
-    on, c = _On(ws, stream), _dims(dims)
+    c, dev = _dims(dims), _device_of(ws, "ws")
     T, A, d, E = c.T, c.T * c.K, c.d_model, c.E
-    dxp, xb = on.either(dx, T * d, "dx", None, True)
-    dwp, wb = on.either(dWr, d * E, "dWr", None, True)
-    on.call("moe_route_backward", ctypes.byref(c), on.ptr(x, T * d, "x", BF16, True), on.ptr(Wr, d * E, "Wr", BF16, True),
-            on.ptr(logits, T * E, "logits", F32, True), on.ptr(topk_idx, A, "topk_idx", I32, True),
-            on.ptr(topk_w, A, "topk_w", F32, True), on.ptr(dtopk_w, A, "dtopk_w", F32, True),
-            on.ptr(counts, E, "counts", I32, True), aux_coef, z_coef, on.ptr(dx_perm, A * d, "dx_perm", BF16, True),
-            on.ptr(inv, A, "inv", I32, True), dxp, xb, dwp, wb, on.ptr(dlogits, T * E, "dlogits", F32, True),
-            on.ptr(ws, 0, "ws", torch.uint8), ws.numel())
+    xt = BF16 if dx is None else _float_type(dx, "dx")
+    wt = BF16 if dWr is None else _float_type(dWr, "dWr")
+    _launch((_lib or load()).moe_route_backward, "moe_route_backward", dev, stream, (
+        ctypes.byref(c), _may(x, T * d, BF16, dev, "x"), _may(Wr, d * E, BF16, dev, "Wr"), _may(logits, T * E, F32, dev, "logits"),
+        _may(topk_idx, A, I32, dev, "topk_idx"), _may(topk_w, A, F32, dev, "topk_w"), _may(dtopk_w, A, F32, dev, "dtopk_w"),
+        _may(counts, E, I32, dev, "counts"), aux_coef, z_coef, _may(dx_perm, A * d, BF16, dev, "dx_perm"),
+        _may(inv, A, I32, dev, "inv"), _may(dx, T * d, xt, dev, "dx"), xt is BF16, _may(dWr, d * E, wt, dev, "dWr"), wt is BF16,
+        _may(dlogits, T * E, F32, dev, "dlogits"), _need(ws, 0, torch.uint8, dev, "ws"), ws.numel()))
 
 
 def alloc_train_workspace(dims, device="cuda") -> torch.Tensor:
