@@ -14,7 +14,10 @@
 //
 // Every product is D[256 x 256] tiles of a CTA pair: CTA r holds the M half r
 // of A and the N half r of B, 64-deep k-blocks of 16 KB each in a ring; the
-// leader issues 256 x 256 x 16 MMAs into two TMEM accumulators in turn.  What
+// leader issues 256 x 256 x 16 MMAs into two TMEM accumulators in turn.  A
+// group's last tile of at most 128 rows takes MMAs of M = 128 and half of A;
+// a CTA's 64 rows are then in TMEM lanes 0-63 with the tile's first 128 columns
+// and in lanes 64-127 with the others.  What
 // differs is which side of an operand is contiguous in memory: tcgen05 takes
 // either from shared memory, so no operand is ever transposed:
 //   K contiguous  (X, dY, dG|dU; W2 and W1, W3 as transposed weights): boxes
@@ -103,6 +106,7 @@ struct Args {
 struct Maps {
     CUtensorMap a[kProducts];
     CUtensorMap b[kProducts];
+    CUtensorMap ah[2];         // token-major: a[] in boxes of 64 rows
     CUtensorMap c[kProducts];  // weight gradients: the outputs [G, M, N], boxes of 128 bytes x 32 rows
 };
 
@@ -172,6 +176,7 @@ struct Tile {
     int g, j, n, m;    // group, product, column tile, row tile
     int64_t row0;      // token-major: first token row; weight gradient: first row of the reduction
     int rows;          // token-major: valid rows of the tile (<= 256)
+    bool half;         // M = 128
     int kb;            // k-blocks
     int k_tail;        // weight gradient: valid rows of the last k-block
 };
@@ -211,11 +216,13 @@ __device__ __forceinline__ Tile decode(const Args& a, const Sched& sc, int tile)
     if (WG) {
         t.row0 = sc.off[t.g];
         t.rows = 256;
+        t.half = false;
         t.kb = (rows + kBK - 1) / kBK;
         t.k_tail = rows - (t.kb - 1) * kBK;
     } else {
         t.row0 = sc.off[t.g] + t.m * 256;
         t.rows = min(256, rows - t.m * 256);
+        t.half = t.rows <= 128;
         t.kb = a.kb_all;
         t.k_tail = kBK;
     }
@@ -362,8 +369,9 @@ struct WeightStore {
 };
 
 // A warp's part of a 256-column sub-tile: 32 rows (`rows` of them valid) from
-// output row `row0`, columns from `col0` up to the width N: 128 of them, 64 of
-// each projection for E_GATE.  `taddr` is its first accumulator column.
+// output row `row0`, `n` chunks of 32 columns from `col0` up to the width N
+// (E_GATE: of each projection; U's accumulator columns are 64 behind G's).
+// `taddr` is its first accumulator column.
 // E_DGATE reads the saved projections at the same places; `load` (before the
 // accumulator is ready) fetches the first 32 columns' worth.
 template <int EPI>
@@ -388,28 +396,28 @@ struct Epilogue {
         }
     }
 
-    __device__ __forceinline__ void run(const Product& p, uint32_t taddr, int64_t row0, int rows, int col0) {
+    __device__ __forceinline__ void run(const Product& p, uint32_t taddr, int64_t row0, int rows, int col0, int n) {
         if constexpr (EPI == E_GATE) {
 #pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-                const int col = col0 + 32 * q, n = (p.N - col) / 8;
+            for (int q = 0; q < n; ++q) {
+                const int col = col0 + 32 * q, chunks = (p.N - col) / 8;
                 if (col >= p.N) return;
                 float v[32], w[32];
                 tmem_ld32(taddr + static_cast<uint32_t>(32 * q), v);
-                tmem_ld32(taddr + static_cast<uint32_t>(128 + 32 * q), w);
+                tmem_ld32(taddr + static_cast<uint32_t>(64 + 32 * q), w);
                 uint8_t* gu = reinterpret_cast<uint8_t*>(static_cast<bf16*>(p.out) + row0 * p.ld + col);
                 stage_bf16(stg, lane, v);
-                flush(stg, lane, gu, p.ld * 2, rows, n);
+                flush(stg, lane, gu, p.ld * 2, rows, chunks);
                 stage_bf16(stg, lane, w);
-                flush(stg, lane, gu + static_cast<int64_t>(p.N) * 2, p.ld * 2, rows, n);
+                flush(stg, lane, gu + static_cast<int64_t>(p.N) * 2, p.ld * 2, rows, chunks);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= sigmoid(v[i]) * w[i];
                 stage_bf16(stg, lane, v);
-                flush(stg, lane, reinterpret_cast<uint8_t*>(a.h + row0 * p.N + col), static_cast<int64_t>(p.N) * 2, rows, n);
+                flush(stg, lane, reinterpret_cast<uint8_t*>(a.h + row0 * p.N + col), static_cast<int64_t>(p.N) * 2, rows, chunks);
             }
         } else if constexpr (EPI == E_DGATE) {
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < n; ++q) {
                 const int col = col0 + 32 * q, c = col + 8 * (lane & 3);
                 if (col >= p.N) return;
                 float acc[4][8];
@@ -436,7 +444,7 @@ struct Epilogue {
                 uint4 gn[4], un[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) gn[i] = g[i], un[i] = u[i];
-                if (q < 3 && col + 32 < p.N) load(p, row0, rows, col + 32);
+                if (q + 1 < n && col + 32 < p.N) load(p, row0, rows, col + 32);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = 8 * i + (lane >> 2);
@@ -461,7 +469,7 @@ struct Epilogue {
             const int bytes = as_bf16 ? 2 : 4;
             uint8_t* out = static_cast<uint8_t*>(p.out) + row0 * p.ld * bytes;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < n; ++q) {
                 const int col = col0 + 32 * q;
                 if (col >= p.N) return;
                 float v[32];
@@ -597,8 +605,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 const Tile t = decode<WG>(a, sc, tile);
                 const int col0 = t.n * SUB * kSubCols;
                 const int subs = min(SUB, (a.p[t.j].N - col0 + kSubCols - 1) / kSubCols);
-                const int n0 = col0 + (EPI == E_GATE ? 0 : 128 * static_cast<int>(rank));
-                const uint32_t bytes = static_cast<uint32_t>(1 + subs) * kOperand;
+                const int n0 = col0 + (EPI == E_GATE ? 64 : 128) * static_cast<int>(rank);
+                const uint32_t bytes = static_cast<uint32_t>(subs) * kOperand + (t.half ? kOperand / 2 : kOperand);
                 for (int kb = 0; kb < t.kb; ++kb) {
                     if (!wait_or_abort(&empty[s], ph ^ 1u, a, DEV_TIMEOUT_PRODUCER_EMPTY, abort_flag, peer_abort)) {
                         ok = false;
@@ -630,12 +638,16 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                     } else {
                         const int second = kb >= a.kb_first ? 1 : 0;
                         const int k0 = (kb - (second ? a.kb_first : 0)) * kBK;
-                        load_2d(&maps.a[second], sa, bar, k0, static_cast<int>(t.row0) + 128 * static_cast<int>(rank));
-                        const CUtensorMap* b = EPI == E_GATE ? &maps.b[rank] : &maps.b[second];
+                        load_2d(t.half ? &maps.ah[second] : &maps.a[second], sa, bar, k0,
+                                static_cast<int>(t.row0) + (t.half ? 64 : 128) * static_cast<int>(rank));
+                        const CUtensorMap* b = &maps.b[second];
                         for (int j = 0; j < subs; ++j) {
                             const uint32_t sb = sa + (1 + j) * kOperand;
                             const int n = n0 + kSubCols * j;
-                            if (B_MN) {
+                            if (EPI == E_GATE) {  // the same 64 columns of both projections
+                                load_3d(&maps.b[0], sb, bar, n, k0, t.g);
+                                load_3d(&maps.b[1], sb + 8192, bar, n, k0, t.g);
+                            } else if (B_MN) {
                                 load_3d(b, sb, bar, n, k0, t.g);
                                 load_3d(b, sb + 8192, bar, n + 64, k0, t.g);
                             } else {
@@ -659,7 +671,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer (leader)
         // idesc: D fp32, A and B bf16, bits 15 and 16 set where A, B are M-, N-contiguous
-        constexpr uint32_t idesc = umma_idesc_bf16(256, 256) | (WG ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
+        constexpr uint32_t major = (WG ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
         uint32_t s = 0, ph = 0, tail_ph = 0, uses1 = 0;  // uses1: tiles that filled the second of two sub-tiles
         int it = 0;
         bool ok = true;
@@ -678,7 +690,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             return steps;
         };
         // Stage `st`'s k-block into accumulator `buf` with sub-tile j of B.
-        auto multiply = [&](uint32_t st, int j, int buf, int steps, bool first) {
+        auto multiply = [&](const Tile& t, uint32_t st, int j, int buf, int steps, bool first) {
+            const uint32_t idesc = (t.half ? umma_idesc_bf16(128, 256) : umma_idesc_bf16(256, 256)) | major;
             const uint32_t stage = smem_u32(smem + st * kStageBytes), d_tmem = tmem_base + static_cast<uint32_t>(buf) * 256u;
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk) {
@@ -708,7 +721,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                         ok = false;
                         break;
                     }
-                    if (lane == 0) multiply(s, 0, 0, kBK / 16, kb == 0);
+                    if (lane == 0) multiply(t, s, 0, 0, kBK / 16, kb == 0);
                     __syncwarp();
                     ++kb;
                     if (++s == kStages) { s = 0; ph ^= 1u; }
@@ -718,7 +731,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 if (lane == 0) {
                     uint32_t st = s0;
                     for (int b = 0; b < kb; ++b) {
-                        multiply(st, 1, 1, kBK / 16, b == 0);
+                        multiply(t, st, 1, 1, kBK / 16, b == 0);
                         commit_pair(&empty[st]);
                         if (++st == kStages) st = 0;
                     }
@@ -732,7 +745,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                     break;
                 }
                 if (lane == 0) {
-                    for (int j = 0; j < subs; ++j) multiply(s, j, buf0 + j, steps, kb == 0);
+                    for (int j = 0; j < subs; ++j) multiply(t, s, j, buf0 + j, steps, kb == 0);
                     commit_pair(&empty[s]);
                 }
                 __syncwarp();
@@ -775,8 +788,9 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         }
     } else {
         // ---------------------------------------------------- epilogue (both CTAs)
-        // Warp quarter q holds rows 32 q .. of this CTA's 128; the two warps of
-        // a quarter take the two column halves.
+        // Warp quarter q holds rows 32 q .. of this CTA's 128 and the two warps of
+        // a quarter take the two column halves; of M = 128, quarters q and q + 2
+        // hold rows 32 q .. of 64 and a column half each, shared by their warps.
         const int q = warp & 3, half = (warp - 2) >> 2;
         const uint32_t leader_tempty = peer_addr(smem_u32(tempty), 0);
         uint8_t* const stg = smem + kRingBytes + (warp - 2) * staging_of(WG);
@@ -786,14 +800,18 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         bool ok = true;
         for (int tile = pair; ok && tile < sc.total; tile += npairs) {
             const Tile t = decode<WG>(a, sc, tile);
-            const int r0 = static_cast<int>(rank) * 128 + q * 32;  // this warp's first row of the tile
+            const int r0 = t.half ? static_cast<int>(rank) * 64 + (q & 1) * 32 : static_cast<int>(rank) * 128 + q * 32;
+            // its first column of a sub-tile, that column's accumulator, and its 32-column chunks
+            const int part = t.half ? (q >> 1) * (kSubCols / 2) + half * (kSubCols / 4) : half * (kSubCols / 2);
+            const int part_acc = t.half ? half * (kSubCols / 4) : half * 128;
+            const int part_n = (kSubCols / 64) / (t.half ? 2 : 1);
             const Product& p = a.p[t.j];
             const int rows = max(0, min(32, (WG ? p.M - t.m * 256 : t.rows) - r0));
             const int64_t row0 = WG ? static_cast<int64_t>(t.g) * p.M + t.m * 256 + r0 : t.row0 + r0;
             const int tile_col = t.n * SUB * kSubCols;
             const int subs = SUB == 1 ? 1 : min(SUB, (p.N - tile_col + kSubCols - 1) / kSubCols);
             for (int j = 0; j < subs; ++j) {
-                const int col0 = tile_col + j * kSubCols + half * (kSubCols / 2);
+                const int col0 = tile_col + j * kSubCols + part;
                 if (WG && t.kb == 0) {
                     epi.zero(p, row0, rows, col0);
                     continue;
@@ -809,7 +827,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 }
                 tc_fence_after();
                 const uint32_t taddr = tmem_base + static_cast<uint32_t>(buf) * 256u + (static_cast<uint32_t>(q * 32) << 16) +
-                                       static_cast<uint32_t>(half * (kSubCols / 2));
+                                       static_cast<uint32_t>(part_acc);
                 if constexpr (WG) {
                     WeightStore<EPI> w;
                     w.fetch(taddr);
@@ -818,7 +836,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                     if (lane == 0) arrive_cluster(leader_tempty + 8u * buf);
                     if (mine) w.store(&maps.c[t.j], stg, lane, a.out_bf16, p.N, col0, t.m * 256 + r0, t.g);
                 } else {
-                    if (mine) epi.run(p, taddr, row0, rows, col0);
+                    if (mine) epi.run(p, taddr, row0, rows, col0, part_n);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) arrive_cluster(leader_tempty + 8u * buf);
@@ -1003,10 +1021,11 @@ int launch_train_gate(const bf16* x, const int32_t* off, int64_t rows, int E, in
                       const bf16* W3, bf16* gu, bf16* h, int* status, cudaStream_t st) {
     Maps m;
     std::memset(&m, 0, sizeof(m));
-    if (!map_matrix(&m.a[0], x, rows, d, d, 128) || !map_weights(&m.b[0], W1, E, d, f, 64) ||
+    if (!map_matrix(&m.a[0], x, rows, d, d, 128) || !map_matrix(&m.ah[0], x, rows, d, d, 64) || !map_weights(&m.b[0], W1, E, d, f, 64) ||
         !map_weights(&m.b[1], W3, E, d, f, 64))
         return -3;
     m.a[1] = m.a[0];
+    m.ah[1] = m.ah[0];
     Args a = token_major(off, rows, E, f, 2 * static_cast<int64_t>(f), gu, ceil_div(d, kBK), ceil_div(d, kBK), status);
     a.h = h;
     return launch<E_GATE, true>(m, a, a.kb_all, row_tile_bound(rows, E), st);
@@ -1016,8 +1035,9 @@ int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, in
                       int* status, cudaStream_t st) {
     Maps m;
     std::memset(&m, 0, sizeof(m));
-    if (!map_matrix(&m.a[0], h, rows, f, f, 128) || !map_weights(&m.b[0], W2, E, f, d, 64)) return -3;
+    if (!map_matrix(&m.a[0], h, rows, f, f, 128) || !map_matrix(&m.ah[0], h, rows, f, f, 64) || !map_weights(&m.b[0], W2, E, f, d, 64)) return -3;
     m.a[1] = m.a[0];
+    m.ah[1] = m.ah[0];
     m.b[1] = m.b[0];
     Args a = token_major(off, rows, E, d, d, y, ceil_div(f, kBK), ceil_div(f, kBK), status);
     return launch<E_F32, true>(m, a, a.kb_all, row_tile_bound(rows, E), st);
@@ -1027,8 +1047,9 @@ int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, 
                        const bf16* gu, bf16* dgu, int* status, cudaStream_t st) {
     Maps m;
     std::memset(&m, 0, sizeof(m));
-    if (!map_matrix(&m.a[0], dy, rows, d, d, 128) || !map_weights(&m.b[0], W2, E, f, d, 128)) return -3;
+    if (!map_matrix(&m.a[0], dy, rows, d, d, 128) || !map_matrix(&m.ah[0], dy, rows, d, d, 64) || !map_weights(&m.b[0], W2, E, f, d, 128)) return -3;
     m.a[1] = m.a[0];
+    m.ah[1] = m.ah[0];
     m.b[1] = m.b[0];
     Args a = token_major(off, rows, E, f, 2 * static_cast<int64_t>(f), dgu, ceil_div(d, kBK), ceil_div(d, kBK), status);
     a.gu = gu;
@@ -1041,6 +1062,7 @@ int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, in
     std::memset(&m, 0, sizeof(m));
     const int64_t ld = 2 * static_cast<int64_t>(f);
     if (!map_matrix(&m.a[0], dgu, rows, f, ld, 128) || !map_matrix(&m.a[1], dgu + f, rows, f, ld, 128) ||
+        !map_matrix(&m.ah[0], dgu, rows, f, ld, 64) || !map_matrix(&m.ah[1], dgu + f, rows, f, ld, 64) ||
         !map_weights(&m.b[0], W1, E, d, f, 128) || !map_weights(&m.b[1], W3, E, d, f, 128))
         return -3;
     Args a = token_major(off, rows, E, d, d, dx, ceil_div(f, kBK), 2 * ceil_div(f, kBK), status);
