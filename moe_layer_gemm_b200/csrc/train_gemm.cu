@@ -669,94 +669,93 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 for (int i = 0; i < kStages; ++i) store_cluster(rec + 4u * (4 + kMaxStages + i), use_bytes[i]);
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer (leader)
-        // idesc: D fp32, A and B bf16, bits 15 and 16 set where A, B are M-, N-contiguous
-        constexpr uint32_t major = (WG ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
-        uint32_t s = 0, ph = 0, tail_ph = 0, uses1 = 0;  // uses1: tiles that filled the second of two sub-tiles
-        int it = 0;
-        bool ok = true;
-        // Wait until k-block kb of the tile is in stage s of both CTAs, a tail's
-        // rows behind the group cleared; the 16-k steps to multiply, 0: abort.
-        auto arrived = [&](const Tile& t, int kb) -> int {
-            int steps = kBK / 16;
-            if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
-                const uint32_t tph = (tail_ph >> s) & 1u;
-                tail_ph ^= 1u << s;
-                if (!warp_wait<true>(&clear[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
-                steps = (t.k_tail + 15) / 16;
-            }
-            if (!warp_wait(&full[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
-            tc_fence_after();
-            return steps;
-        };
-        // Stage `st`'s k-block into accumulator `buf` with sub-tile j of B.
-        auto multiply = [&](const Tile& t, uint32_t st, int j, int buf, int steps, bool first) {
-            const uint32_t idesc = (t.half ? umma_idesc_bf16(128, 256) : umma_idesc_bf16(256, 256)) | major;
-            const uint32_t stage = smem_u32(smem + st * kStageBytes), d_tmem = tmem_base + static_cast<uint32_t>(buf) * 256u;
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-                if (WG && kk >= steps) break;
-                const uint32_t sb = stage + (1 + j) * kOperand;
-                const uint64_t da = WG ? desc_mn(stage + kk * 2048) : umma_desc_sw128(stage + kk * 32);
-                const uint64_t db = B_MN ? desc_mn(sb + kk * 2048) : umma_desc_sw128(sb + kk * 32);
-                mma_pair(d_tmem, da, db, idesc, (!first || kk > 0) ? 1u : 0u);
-            }
-        };
-        for (int tile = pair; ok && leader && tile < sc.total; tile += npairs) {
-            const Tile t = decode<WG>(a, sc, tile);
-            if (t.kb == 0) continue;
-            const int subs = SUB == 1 ? 1 : min(SUB, (a.p[t.j].N - t.n * SUB * kSubCols + kSubCols - 1) / kSubCols);
-            int kb = 0;
-            const int buf0 = SUB == 1 ? it & 1 : 0;
-            const uint32_t use = static_cast<uint32_t>(SUB == 1 ? it >> 1 : it);
-            if (!warp_wait<true>(&tempty[buf0], (use & 1u) ^ 1u, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
-            tc_fence_after();
-            if (SUB == 2 && subs == 2) {
-                // the second accumulator may still be read: go ahead in the first
-                // with the k-blocks that the ring holds (whole ones, before any tail)
-                const uint32_t s0 = s, want = (uses1 & 1u) ^ 1u;
-                while (kb < kStages && kb < t.kb - 1) {
-                    if (__all_sync(0xffffffffu, try_wait_cluster(&tempty[1], want))) break;
-                    if (!arrived(t, kb)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) multiply(t, s, 0, 0, kBK / 16, kb == 0);
-                    __syncwarp();
-                    ++kb;
-                    if (++s == kStages) { s = 0; ph ^= 1u; }
+        // ---------------------------------------------------- MMA issuer (one thread of the leader)
+        if (leader && lane == 0) {
+            // idesc: D fp32, A and B bf16, bits 15 and 16 set where A, B are M-, N-contiguous
+            constexpr uint32_t major = (WG ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
+            // descriptors of the ring's first byte; a stage, a sub-tile and a step of 16 k add to their address field
+            const uint32_t ring = smem_u32(smem);
+            const uint64_t desc_a = WG ? desc_mn(ring) : umma_desc_sw128(ring);
+            const uint64_t desc_b = (B_MN ? desc_mn(ring) : umma_desc_sw128(ring)) + (kOperand >> 4);
+            uint32_t s = 0, ph = 0, tail_ph = 0, uses1 = 0;  // uses1: tiles that filled the second of two sub-tiles
+            int it = 0;
+            bool ok = true;
+            // Wait until k-block kb of the tile is in stage s of both CTAs, a tail's
+            // rows behind the group cleared; the 16-k steps to multiply, 0: abort.
+            auto arrived = [&](const Tile& t, int kb) -> int {
+                int steps = kBK / 16;
+                if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
+                    const uint32_t tph = (tail_ph >> s) & 1u;
+                    tail_ph ^= 1u << s;
+                    if (!wait_or_abort<true>(&clear[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
+                    steps = (t.k_tail + 15) / 16;
                 }
-                if (!ok || !warp_wait<true>(&tempty[1], want, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
+                if (!wait_or_abort(&full[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
                 tc_fence_after();
-                if (lane == 0) {
+                return steps;
+            };
+            // Stage `st`'s k-block into accumulator `buf` with sub-tile j of B.
+            auto multiply = [&](uint32_t idesc, uint32_t st, int j, int buf, int steps, bool first) {
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf) * 256u;
+                const uint64_t da = desc_a + st * (kStageBytes >> 4);
+                const uint64_t db = desc_b + st * (kStageBytes >> 4) + static_cast<uint32_t>(j) * (kOperand >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk) {
+                    if (WG && kk >= steps) break;
+                    mma_pair(d_tmem, da + kk * ((WG ? 2048 : 32) >> 4), db + kk * ((B_MN ? 2048 : 32) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
+                }
+            };
+            for (int tile = pair; ok && tile < sc.total; tile += npairs) {
+                const Tile t = decode<WG>(a, sc, tile);
+                if (t.kb == 0) continue;
+                const uint32_t idesc = (t.half ? umma_idesc_bf16(128, 256) : umma_idesc_bf16(256, 256)) | major;
+                const int subs = SUB == 1 ? 1 : min(SUB, (a.p[t.j].N - t.n * SUB * kSubCols + kSubCols - 1) / kSubCols);
+                int kb = 0;
+                const int buf0 = SUB == 1 ? it & 1 : 0;
+                const uint32_t use = static_cast<uint32_t>(SUB == 1 ? it >> 1 : it);
+                if (!wait_or_abort<true>(&tempty[buf0], (use & 1u) ^ 1u, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
+                tc_fence_after();
+                if (SUB == 2 && subs == 2) {
+                    // the second accumulator may still be read: go ahead in the first
+                    // with the k-blocks that the ring holds (whole ones, before the last)
+                    const uint32_t s0 = s, want = (uses1 & 1u) ^ 1u;
+                    while (kb < kStages && kb < t.kb - 1 && !try_wait_cluster(&tempty[1], want)) {
+                        if (!arrived(t, kb)) {
+                            ok = false;
+                            break;
+                        }
+                        multiply(idesc, s, 0, 0, kBK / 16, kb == 0);
+                        ++kb;
+                        if (++s == kStages) { s = 0; ph ^= 1u; }
+                    }
+                    if (!ok || !wait_or_abort<true>(&tempty[1], want, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
+                    tc_fence_after();
                     uint32_t st = s0;
                     for (int b = 0; b < kb; ++b) {
-                        multiply(t, st, 1, 1, kBK / 16, b == 0);
+                        multiply(idesc, st, 1, 1, kBK / 16, b == 0);
                         commit_pair(&empty[st]);
                         if (++st == kStages) st = 0;
                     }
                 }
-                __syncwarp();
-            }
-            for (; kb < t.kb; ++kb) {
-                const int steps = arrived(t, kb);
-                if (!steps) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    for (int j = 0; j < subs; ++j) multiply(t, s, j, buf0 + j, steps, kb == 0);
+                for (; kb < t.kb; ++kb) {
+                    const int steps = arrived(t, kb);
+                    if (!steps) {
+                        ok = false;
+                        break;
+                    }
+                    multiply(idesc, s, 0, buf0, steps, kb == 0);
+                    if (SUB == 2 && subs == 2) {
+                        if (kb == t.kb - 1) commit_pair(&tfull[0]);  // its epilogue runs under the last MMAs
+                        multiply(idesc, s, 1, 1, steps, kb == 0);
+                    }
                     commit_pair(&empty[s]);
+                    if (++s == kStages) { s = 0; ph ^= 1u; }
                 }
-                __syncwarp();
-                if (++s == kStages) { s = 0; ph ^= 1u; }
+                if (ok) commit_pair(&tfull[SUB == 2 && subs == 2 ? 1 : buf0]);
+                ++it;
+                uses1 += subs == 2 ? 1u : 0u;
             }
-            if (ok && lane == 0)
-                for (int j = 0; j < subs; ++j) commit_pair(&tfull[buf0 + j]);
-            ++it;
-            uses1 += subs == 2 ? 1u : 0u;
-        }
-        if (leader && lane == 0) {  // every MMA issued is complete before TMEM is freed
+            // every MMA issued is complete before TMEM is freed
             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                          ::"r"(smem_u32(drain)) : "memory");
             mbar_drain(drain, 0, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
