@@ -245,10 +245,15 @@ __device__ __forceinline__ void unpack8(const uint4& q, float* v) {
     v[4] = bf_lo(q.z), v[5] = bf_hi(q.z), v[6] = bf_lo(q.w), v[7] = bf_hi(q.w);
 }
 
-// Logistic function with the fast exponential and division: what comes of it
-// is rounded to bf16, whose step is 2^15 times their error.  For x below -88
-// the exponential overflows to infinity and the quotient is 0, its limit.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// Logistic function with the approximate reciprocal and exponential: what
+// comes of it is rounded to bf16, whose step is 2^14 times their error.  For x
+// below -88 the exponential overflows to infinity, whose reciprocal is 0, the
+// limit.
+__device__ __forceinline__ float sigmoid(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
+    return r;
+}
 
 // A wait that gives up after a.wait_limit polls; its failure, or an abort
 // seen, stops both CTAs of the pair.
@@ -453,9 +458,10 @@ struct Epilogue {
                     unpack8(un[i], uv);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        const float sg = sigmoid(gv[x]);
-                        dg[x] = acc[i][x] * uv[x] * sg * (1.0f + gv[x] * (1.0f - sg));
-                        du[x] = acc[i][x] * gv[x] * sg;
+                        const float sg = sigmoid(gv[x]), silu = gv[x] * sg;
+                        // s (1 + g (1 - s)) = s + g s - g s s
+                        dg[x] = acc[i][x] * uv[x] * (sg + fmaf(-silu, sg, silu));
+                        du[x] = acc[i][x] * silu;
                     }
                     if (r < rows && c < p.N) {
                         bf16* dst = static_cast<bf16*>(p.out) + (row0 + r) * p.ld + c;
