@@ -63,10 +63,6 @@ namespace {
 
 constexpr int kBK = 64;
 constexpr uint32_t kOperand = 16384u;  // one CTA's half of an operand: 128 x 64 bf16
-constexpr uint32_t kRingBytes = 12 * kOperand;
-// Output staging of an epilogue warp.  (Weight gradients need no table of first
-// tiles, so 4 KB fit beside the ring.)
-constexpr int staging_of(bool wgrad) { return wgrad ? 4096 : 2048; }
 constexpr uint32_t kTmemCols = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;   // weight gradients: one more warp, which clears tails
@@ -76,6 +72,12 @@ constexpr int kMaxStages = 6;
 constexpr int kRaster = 3;  // tile columns walked together: the operands of the ~74 tiles in flight stay in L2
 
 enum Epi : int { E_GATE, E_F32, E_DGATE, E_BF16, E_WGRAD };
+
+// Operand ring, and output staging of an epilogue warp.  The saved projections'
+// gradient stages two outputs beside the sums that it turns round; weight
+// gradients need no table of first tiles, so their 4 KB fit beside the ring.
+constexpr uint32_t ring_of(int epi) { return (epi == E_DGATE ? 10 : 12) * kOperand; }
+constexpr int staging_of(int epi) { return epi == E_DGATE ? 6144 : (epi == E_WGRAD ? 4096 : 2048); }
 
 // A weight gradient [M, N] of every group, rows of ld elements.
 struct Product {
@@ -107,7 +109,9 @@ struct Maps {
     CUtensorMap a[kProducts];
     CUtensorMap b[kProducts];
     CUtensorMap ah[2];         // token-major: a[] in boxes of 64 rows
-    CUtensorMap c[kProducts];  // weight gradients: the outputs [G, M, N], boxes of 128 bytes x 32 rows
+    // outputs that leave by TMA: weight gradients [G, M, N] in boxes of 128 bytes x
+    // 32 rows, E_DGATE's two in boxes of 64 bytes x 32 rows
+    CUtensorMap c[kProducts];
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -382,6 +386,7 @@ struct WeightStore {
 template <int EPI>
 struct Epilogue {
     const Args& a;
+    const CUtensorMap* c;  // E_DGATE: the two outputs
     uint8_t* stg;
     int lane;
     uint4 g[EPI == E_DGATE ? 4 : 1], u[EPI == E_DGATE ? 4 : 1];
@@ -423,7 +428,7 @@ struct Epilogue {
         } else if constexpr (EPI == E_DGATE) {
 #pragma unroll 1
             for (int q = 0; q < n; ++q) {
-                const int col = col0 + 32 * q, c = col + 8 * (lane & 3);
+                const int col = col0 + 32 * q, cc = col + 8 * (lane & 3);
                 if (col >= p.N) return;
                 float acc[4][8];
                 {
@@ -450,6 +455,14 @@ struct Epilogue {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) gn[i] = g[i], un[i] = u[i];
                 if (q + 1 < n && col + 32 < p.N) load(p, row0, rows, col + 32);
+                // 32 rows of the tile leave as one TMA store of each gradient (the boxes'
+                // 64-byte swizzle is the staging's), fewer row by row: a box would
+                // reach into the next group
+                uint8_t* const out = stg + 2048;
+                if (rows == 32) {
+                    if (lane == 0) bulk_wait_read<0>();  // the chunk before has been read
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = 8 * i + (lane >> 2);
@@ -463,10 +476,22 @@ struct Epilogue {
                         dg[x] = acc[i][x] * uv[x] * (sg + fmaf(-silu, sg, silu));
                         du[x] = acc[i][x] * silu;
                     }
-                    if (r < rows && c < p.N) {
-                        bf16* dst = static_cast<bf16*>(p.out) + (row0 + r) * p.ld + c;
+                    if (rows == 32) {
+                        *chunk_at(out, r, lane & 3) = pack8(dg);
+                        *chunk_at(out + 2048, r, lane & 3) = pack8(du);
+                    } else if (r < rows && cc < p.N) {
+                        bf16* dst = static_cast<bf16*>(p.out) + (row0 + r) * p.ld + cc;
                         *reinterpret_cast<uint4*>(dst) = pack8(dg);
                         *reinterpret_cast<uint4*>(dst + p.N) = pack8(du);
+                    }
+                }
+                if (rows == 32) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&c[0], out, col, static_cast<int32_t>(row0));
+                        tma_store_2d(&c[1], out + 2048, col, static_cast<int32_t>(row0));
+                        bulk_commit();
                     }
                 }
             }
@@ -517,11 +542,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EPI == E_WGRAD ? kTh
 train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     constexpr bool WG = EPI == E_WGRAD;
     constexpr uint32_t kStageBytes = (1 + SUB) * kOperand;
+    constexpr uint32_t kRingBytes = ring_of(EPI);
     constexpr int kStages = kRingBytes / kStageBytes;
     constexpr int kSubCols = EPI == E_GATE ? 128 : 256;  // output columns of a sub-tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes + kEpiWarps * staging_of(WG));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRingBytes + kEpiWarps * staging_of(EPI));
     uint64_t* empty = full + kStages;
     uint64_t* tail = empty + kStages;
     uint64_t* clear = tail + kStages;
@@ -798,8 +824,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
         // hold rows 32 q .. of 64 and a column half each, shared by their warps.
         const int q = warp & 3, half = (warp - 2) >> 2;
         const uint32_t leader_tempty = peer_addr(smem_u32(tempty), 0);
-        uint8_t* const stg = smem + kRingBytes + (warp - 2) * staging_of(WG);
-        Epilogue<EPI> epi{a, stg, lane};
+        uint8_t* const stg = smem + kRingBytes + (warp - 2) * staging_of(EPI);
+        Epilogue<EPI> epi{a, maps.c, stg, lane};
         int it = 0;
         uint32_t uses1 = 0;
         bool ok = true;
@@ -852,7 +878,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 uses1 += subs == 2 ? 1u : 0u;
             }
         }
-        if (WG && lane == 0) bulk_wait_all();
+        if ((WG || EPI == E_DGATE) && lane == 0) bulk_wait_all();
     }
 
     // No copy is in flight when the pair ends.  A complete run issued the same
@@ -939,19 +965,30 @@ bool map_output(CUtensorMap* m, void* base, bool as_bf16, int64_t mats, int64_t 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Output rows [rows, cols] of bf16 with stride ld, boxes of 64 bytes x 32 rows.
+bool map_rows_out(CUtensorMap* m, bf16* base, int64_t rows, int64_t cols, int64_t ld) {
+    auto enc = map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    cuuint32_t box[2] = {32u, 32u}, es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-constexpr size_t smem_of(bool wgrad) {
-    return 1024 + kRingBytes + kEpiWarps * staging_of(wgrad) + (4 * kMaxStages + 6) * 8 + 8 + (4 + 2 * kMaxStages) * 4 +
-           (wgrad ? 1 : 2) * (kMaxGroups + 1) * 4;
+constexpr size_t smem_of(int epi) {
+    return 1024 + ring_of(epi) + kEpiWarps * staging_of(epi) + (4 * kMaxStages + 6) * 8 + 8 + (4 + 2 * kMaxStages) * 4 +
+           (epi == E_WGRAD ? 1 : 2) * (kMaxGroups + 1) * 4;
 }
-static_assert(smem_of(true) <= 232448 && smem_of(false) <= 232448, "227 KB a CTA");
+static_assert(smem_of(E_GATE) <= 232448 && smem_of(E_DGATE) <= 232448 && smem_of(E_WGRAD) <= 232448, "227 KB a CTA");
 
 template <int EPI, bool B_MN, int SUB>
 int launch_sub(const Maps& maps, Args a, int64_t max_tiles, cudaStream_t st) {
     static std::atomic<unsigned long long> attr_done{0};
     const auto kernel = train_gemm_kernel<EPI, B_MN, SUB>;
-    constexpr size_t kSmem = smem_of(EPI == E_WGRAD);
+    constexpr size_t kSmem = smem_of(EPI);
     if (smem_attr_once(reinterpret_cast<const void*>(kernel), static_cast<int>(kSmem), attr_done) != 0) return -3;
     int pairs = num_sms() / 2;
     if (pairs < 1) return -3;
@@ -1052,7 +1089,10 @@ int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, 
                        const bf16* gu, bf16* dgu, int* status, cudaStream_t st) {
     Maps m;
     std::memset(&m, 0, sizeof(m));
-    if (!map_matrix(&m.a[0], dy, rows, d, d, 128) || !map_matrix(&m.ah[0], dy, rows, d, d, 64) || !map_weights(&m.b[0], W2, E, f, d, 128)) return -3;
+    if (!map_matrix(&m.a[0], dy, rows, d, d, 128) || !map_matrix(&m.ah[0], dy, rows, d, d, 64) || !map_weights(&m.b[0], W2, E, f, d, 128) ||
+        !map_rows_out(&m.c[0], dgu, rows, f, 2 * static_cast<int64_t>(f)) ||
+        !map_rows_out(&m.c[1], dgu + f, rows, f, 2 * static_cast<int64_t>(f)))
+        return -3;
     m.a[1] = m.a[0];
     m.ah[1] = m.ah[0];
     m.b[1] = m.b[0];
