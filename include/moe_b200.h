@@ -10,7 +10,9 @@
  *   stats    counts, f_i, P_i, aux = E * sum f_i P_i, the top-K-only balance
  *            statistic and the router z-loss; aux-free bias update
  * moe_layer_forward runs all five on one stream; moe_layer_forward_chunked
- * runs the same layer over token chunks in a chunk-sized workspace.
+ * runs the same layer over token chunks in a chunk-sized workspace.  The
+ * gradients of the steps, and the layer norm in front of them, are in the
+ * section "training".
  *
  * Sources (web pages; cited by title and section):
  *   [P1] "MoE serving essay", dpshk.com/news/3211971

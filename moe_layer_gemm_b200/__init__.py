@@ -1,4 +1,4 @@
-"""B200-native forward pass of one Mixture-of-Experts FFN layer.
+"""B200-native Mixture-of-Experts FFN layer: its forward pass and the calls that train it.
 
 The compute lives in a C-ABI shared library of hand-written sm_100a CUDA
 kernels (``lib/libmoe_b200.so``); this package is its thin ctypes binding
