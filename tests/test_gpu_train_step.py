@@ -186,6 +186,35 @@ def test_numbers_that_name_no_row():
     assert (dl.gather(1, twice[:, :1].long())[:, 0] - g.sum(1)).abs().max() <= 1e-6
 
 
+def test_outputs_left_out():
+    """Every subset of the wanted gradients comes out as with the others, and needs only its own inputs."""
+    s = Step(120, 272, 144, 5, 2, seed=4)
+    s.run()
+    D, G, ws = s.dims, s.grads, s.tws
+    n = int(s.offsets[-1])
+    want = {k: G[k].clone() for k in ("W1", "W3", "W2", "gamma", "beta")}
+    dgu, dx = s.dgu[:n].clone(), s.dx_perm[:n].clone()
+    new = torch.empty_like
+    a = new(s.dgu), new(s.dx_perm)
+    abi.moe_ffn_backward(D, s.dy_perm, None, s.offsets, s.W1, s.W3, s.W2, s.gu, None, a[0], a[1], None, None, None, ws)
+    assert torch.equal(a[0][:n], dgu) and torch.equal(a[1][:n], dx)
+    b = new(s.dgu), new(s.W2)
+    abi.moe_ffn_backward(D, s.dy_perm, None, s.offsets, None, None, s.W2, s.gu, s.h, b[0], None, None, None, b[1], ws)
+    assert torch.equal(b[0][:n], dgu) and torch.equal(b[1], want["W2"])
+    c = new(s.dgu), new(s.W1), new(s.W3)
+    abi.moe_ffn_backward(D, s.dy_perm, s.x_perm, s.offsets, None, None, s.W2, s.gu, None, c[0], None, c[1], c[2], None, ws)
+    assert torch.equal(c[1], want["W1"]) and torch.equal(c[2], want["W3"])
+    db = new(s.beta)
+    abi.moe_layernorm_backward(s.dxn, s.x, s.gamma, s.mean, s.rstd, s.dout, None, None, db, ws)
+    assert torch.equal(db, want["beta"])
+    dWr, dl = new(G["Wr"]), torch.empty(D.T, D.E, dtype=F32, device="cuda")
+    abi.moe_route_backward(D, s.xn, None, s.logits, s.idx, s.w, s.dw, s.counts, AUX, ZC, None, None, None, dWr, dl, ws)
+    assert torch.equal(dWr, G["Wr"])
+    only = new(dl)
+    abi.moe_route_backward(D, None, None, s.logits, s.idx, s.w, s.dw, s.counts, AUX, ZC, None, None, None, None, only, ws)
+    assert torch.equal(only, dl)
+
+
 def test_refused_tensors():
     s = Step(16, 64, 32, 4, 2, seed=1)
     D = s.dims
