@@ -53,6 +53,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -114,6 +115,18 @@ struct Maps {
     CUtensorMap c[kProducts];
 };
 
+// One thread of a converged warp.  The roles that issue copies and MMAs run in
+// whole warps on warp-uniform values, and only these instructions are
+// predicated: their operands are uniform registers, which a branch of one
+// thread would have to fill from vector registers for each of them.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
+}
+template <typename T>
+__device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 __device__ __forceinline__ uint32_t cta_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -142,25 +155,28 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
     return ok != 0;
 }
 // Loads into this CTA's shared memory that complete on a barrier of either CTA.
-__device__ __forceinline__ void load_2d(const CUtensorMap* map, uint32_t dst, uint32_t bar, int32_t x, int32_t y) {
-    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];"
-                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+__device__ __forceinline__ void load_2d(uint32_t one, const CUtensorMap* map, uint32_t dst, uint32_t bar, int32_t x, int32_t y) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];\n\t}"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(one) : "memory");
 }
-__device__ __forceinline__ void load_3d(const CUtensorMap* map, uint32_t dst, uint32_t bar, int32_t x, int32_t y,
-                                        int32_t z) {
-    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3, %4}], [%5];"
-                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+__device__ __forceinline__ void load_3d(uint32_t one, const CUtensorMap* map, uint32_t dst, uint32_t bar, int32_t x,
+                                        int32_t y, int32_t z) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+                 "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];\n\t}"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one) : "memory");
 }
-__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+__device__ __forceinline__ void mma_pair(uint32_t one, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one) : "memory");
 }
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+__device__ __forceinline__ void commit_pair(uint32_t one, uint64_t* bar) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+                 ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)), "r"(one) : "memory");
 }
 
 // Operand whose M or N side is contiguous: two boxes of 64 columns x 64 k
@@ -627,70 +643,79 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     const uint32_t peer_abort = peer_addr(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------ producer (both CTAs)
-            const uint32_t leader_full = peer_addr(smem_u32(full), 0), own_tail = peer_addr(smem_u32(tail), rank);
-            uint32_t s = 0, ph = 0, uses = 0, tails = 0, tail_ph = 0;
-            uint32_t* use_bytes = issued + 4 + kMaxStages * rank;  // this CTA's bytes of each stage's last use
-            bool ok = true;
-            for (int tile = pair; ok && tile < sc.total; tile += npairs) {
-                const Tile t = decode<WG>(a, sc, tile);
-                const int col0 = t.n * SUB * kSubCols;
-                const int subs = min(SUB, (a.p[t.j].N - col0 + kSubCols - 1) / kSubCols);
-                const int n0 = col0 + (EPI == E_GATE ? 64 : 128) * static_cast<int>(rank);
-                const uint32_t bytes = static_cast<uint32_t>(subs) * kOperand + (t.half ? kOperand / 2 : kOperand);
-                for (int kb = 0; kb < t.kb; ++kb) {
-                    if (!wait_or_abort(&empty[s], ph ^ 1u, a, DEV_TIMEOUT_PRODUCER_EMPTY, abort_flag, peer_abort)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = smem_u32(smem + s * kStageBytes);
-                    uint32_t bar = leader_full + 8u * s;
-                    if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
-                        bar = own_tail + 8u * s;
-                        mbar_arrive_expect_tx(&tail[s], bytes);
-                        if (leader) mbar_arrive(&full[s]);
-                        tails |= 1u << s;
-                        tail_ph ^= 1u << s;
-                    } else {
-                        if (leader) mbar_arrive_expect_tx(&full[s], 2 * bytes);
-                        tails &= ~(1u << s);
-                    }
-                    use_bytes[s] = bytes;
-                    if (WG) {
-                        const int y = static_cast<int>(t.row0) + kb * kBK;
-                        const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
-                        load_2d(&maps.a[t.j], sa, bar, m0, y);
-                        load_2d(&maps.a[t.j], sa + 8192, bar, m0 + 64, y);
-                        for (int j = 0; j < subs; ++j) {
-                            const uint32_t sb = sa + (1 + j) * kOperand;
-                            load_2d(&maps.b[t.j], sb, bar, n0 + 256 * j, y);
-                            load_2d(&maps.b[t.j], sb + 8192, bar, n0 + 256 * j + 64, y);
-                        }
-                    } else {
-                        const int second = kb >= a.kb_first ? 1 : 0;
-                        const int k0 = (kb - (second ? a.kb_first : 0)) * kBK;
-                        load_2d(t.half ? &maps.ah[second] : &maps.a[second], sa, bar, k0,
-                                static_cast<int>(t.row0) + (t.half ? 64 : 128) * static_cast<int>(rank));
-                        const CUtensorMap* b = &maps.b[second];
-                        for (int j = 0; j < subs; ++j) {
-                            const uint32_t sb = sa + (1 + j) * kOperand;
-                            const int n = n0 + kSubCols * j;
-                            if (EPI == E_GATE) {  // the same 64 columns of both projections
-                                load_3d(&maps.b[0], sb, bar, n, k0, t.g);
-                                load_3d(&maps.b[1], sb + 8192, bar, n, k0, t.g);
-                            } else if (B_MN) {
-                                load_3d(b, sb, bar, n, k0, t.g);
-                                load_3d(b, sb + 8192, bar, n + 64, k0, t.g);
-                            } else {
-                                load_3d(b, sb, bar, k0, n, t.g);
-                            }
-                        }
-                    }
-                    ++uses;
-                    if (++s == kStages) { s = 0; ph ^= 1u; }
+        // ---------------------------------------------------- producer (both CTAs)
+        const uint32_t one = elect_one();
+        const uint32_t leader_full = peer_addr(smem_u32(full), 0), own_tail = peer_addr(smem_u32(tail), rank);
+        uint32_t s = 0, ph = 0, uses = 0, tails = 0, tail_ph = 0;
+        uint32_t* use_bytes = issued + 4 + kMaxStages * rank;  // this CTA's bytes of each stage's last use
+        bool ok = true;
+        for (int tile = pair; ok && tile < sc.total; tile += npairs) {
+            Tile t = decode<WG>(a, sc, tile);
+            t.j = uniform(t.j);
+            t.g = uniform(t.g);
+            t.m = uniform(t.m);
+            t.n = uniform(t.n);
+            t.kb = uniform(t.kb);
+            t.k_tail = uniform(t.k_tail);
+            const int row0 = uniform(static_cast<int>(t.row0));
+            const bool half = uniform(static_cast<int>(t.half)) != 0;
+            const int col0 = t.n * SUB * kSubCols;
+            const int subs = min(SUB, (a.p[t.j].N - col0 + kSubCols - 1) / kSubCols);
+            const int n0 = col0 + (EPI == E_GATE ? 64 : 128) * static_cast<int>(rank);
+            const uint32_t bytes = static_cast<uint32_t>(subs) * kOperand + (half ? kOperand / 2 : kOperand);
+            for (int kb = 0; kb < t.kb; ++kb) {
+                if (!warp_wait(&empty[s], ph ^ 1u, a, DEV_TIMEOUT_PRODUCER_EMPTY, abort_flag, peer_abort)) {
+                    ok = false;
+                    break;
                 }
+                const uint32_t sa = smem_u32(smem + s * kStageBytes);
+                uint32_t bar = leader_full + 8u * s;
+                if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
+                    bar = own_tail + 8u * s;
+                    if (one) mbar_arrive_expect_tx(&tail[s], bytes);
+                    if (leader && one) mbar_arrive(&full[s]);
+                    tails |= 1u << s;
+                    tail_ph ^= 1u << s;
+                } else {
+                    if (leader && one) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                    tails &= ~(1u << s);
+                }
+                if (one) use_bytes[s] = bytes;
+                if (WG) {
+                    const int y = row0 + kb * kBK;
+                    const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
+                    load_2d(one, &maps.a[t.j], sa, bar, m0, y);
+                    load_2d(one, &maps.a[t.j], sa + 8192, bar, m0 + 64, y);
+                    for (int j = 0; j < subs; ++j) {
+                        const uint32_t sb = sa + (1 + j) * kOperand;
+                        load_2d(one, &maps.b[t.j], sb, bar, n0 + 256 * j, y);
+                        load_2d(one, &maps.b[t.j], sb + 8192, bar, n0 + 256 * j + 64, y);
+                    }
+                } else {
+                    const int second = kb >= a.kb_first ? 1 : 0;
+                    const int k0 = (kb - (second ? a.kb_first : 0)) * kBK;
+                    load_2d(one, half ? &maps.ah[second] : &maps.a[second], sa, bar, k0,
+                            row0 + (half ? 64 : 128) * static_cast<int>(rank));
+                    const CUtensorMap* b = &maps.b[second];
+                    for (int j = 0; j < subs; ++j) {
+                        const uint32_t sb = sa + (1 + j) * kOperand;
+                        const int n = n0 + kSubCols * j;
+                        if (EPI == E_GATE) {  // the same 64 columns of both projections
+                            load_3d(one, &maps.b[0], sb, bar, n, k0, t.g);
+                            load_3d(one, &maps.b[1], sb + 8192, bar, n, k0, t.g);
+                        } else if (B_MN) {
+                            load_3d(one, b, sb, bar, n, k0, t.g);
+                            load_3d(one, b, sb + 8192, bar, n + 64, k0, t.g);
+                        } else {
+                            load_3d(one, b, sb, bar, k0, n, t.g);
+                        }
+                    }
+                }
+                ++uses;
+                if (++s == kStages) { s = 0; ph ^= 1u; }
             }
+        }
+        if (one) {
             // this CTA's own tails have landed (a phase never used counts as complete)
             for (int i = 0; WG && i < kStages; ++i)
                 mbar_drain(&tail[i], ((tail_ph >> i) & 1u) ^ 1u, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
@@ -701,8 +726,20 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 for (int i = 0; i < kStages; ++i) store_cluster(rec + 4u * (4 + kMaxStages + i), use_bytes[i]);
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer (one thread of the leader)
-        if (leader && lane == 0) {
+        // ---------------------------------------------------- MMA issuer (leader)
+        // By the whole warp where a tile has one sub-tile of columns: 60 small experts'
+        // backward takes 960 us, 974 by one thread.  The wide tiles' eight MMAs a k-block
+        // keep the tensor cores fed from one thread, which is the faster there: forward of
+        // the Mixtral-shaped batch 8.16 ms, 8.43 by the warp.
+        constexpr bool kWarp = SUB == 1;
+        if (leader && (kWarp || lane == 0)) {
+            const uint32_t one = kWarp ? elect_one() : 1u;
+            auto wait = [&](auto cluster, uint64_t* bar, uint32_t parity, int code) -> bool {
+                constexpr bool kCluster = decltype(cluster)::value;
+                if (kWarp) return warp_wait<kCluster>(bar, parity, a, code, abort_flag, peer_abort);
+                return wait_or_abort<kCluster>(bar, parity, a, code, abort_flag, peer_abort);
+            };
+            auto same = [&](int v) { return kWarp ? uniform(v) : v; };
             // idesc: D fp32, A and B bf16, bits 15 and 16 set where A, B are M-, N-contiguous
             constexpr uint32_t major = (WG ? (1u << 15) : 0u) | (B_MN ? (1u << 16) : 0u);
             // descriptors of the ring's first byte; a stage, a sub-tile and a step of 16 k add to their address field
@@ -719,10 +756,10 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 if (WG && kb == t.kb - 1 && t.k_tail < kBK) {
                     const uint32_t tph = (tail_ph >> s) & 1u;
                     tail_ph ^= 1u << s;
-                    if (!wait_or_abort<true>(&clear[s], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
+                    if (!wait(std::true_type{}, &clear[s], tph, DEV_TIMEOUT_MMA_FULL)) return 0;
                     steps = (t.k_tail + 15) / 16;
                 }
-                if (!wait_or_abort(&full[s], ph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) return 0;
+                if (!wait(std::false_type{}, &full[s], ph, DEV_TIMEOUT_MMA_FULL)) return 0;
                 tc_fence_after();
                 return steps;
             };
@@ -734,18 +771,20 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
 #pragma unroll
                 for (int kk = 0; kk < kBK / 16; ++kk) {
                     if (WG && kk >= steps) break;
-                    mma_pair(d_tmem, da + kk * ((WG ? 2048 : 32) >> 4), db + kk * ((B_MN ? 2048 : 32) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
+                    mma_pair(one, d_tmem, da + kk * ((WG ? 2048 : 32) >> 4), db + kk * ((B_MN ? 2048 : 32) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
                 }
             };
             for (int tile = pair; ok && tile < sc.total; tile += npairs) {
-                const Tile t = decode<WG>(a, sc, tile);
+                Tile t = decode<WG>(a, sc, tile);
+                t.kb = same(t.kb);
+                t.k_tail = same(t.k_tail);
                 if (t.kb == 0) continue;
-                const uint32_t idesc = (t.half ? umma_idesc_bf16(128, 256) : umma_idesc_bf16(256, 256)) | major;
-                const int subs = SUB == 1 ? 1 : min(SUB, (a.p[t.j].N - t.n * SUB * kSubCols + kSubCols - 1) / kSubCols);
+                const uint32_t idesc = (same(static_cast<int>(t.half)) ? umma_idesc_bf16(128, 256) : umma_idesc_bf16(256, 256)) | major;
+                const int subs = SUB == 1 ? 1 : same(min(SUB, (a.p[t.j].N - t.n * SUB * kSubCols + kSubCols - 1) / kSubCols));
                 int kb = 0;
                 const int buf0 = SUB == 1 ? it & 1 : 0;
                 const uint32_t use = static_cast<uint32_t>(SUB == 1 ? it >> 1 : it);
-                if (!wait_or_abort<true>(&tempty[buf0], (use & 1u) ^ 1u, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
+                if (!wait(std::true_type{}, &tempty[buf0], (use & 1u) ^ 1u, DEV_TIMEOUT_MMA_TEMPTY)) break;
                 tc_fence_after();
                 if (SUB == 2 && subs == 2) {
                     // the second accumulator may still be read: go ahead in the first
@@ -760,12 +799,12 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                         ++kb;
                         if (++s == kStages) { s = 0; ph ^= 1u; }
                     }
-                    if (!ok || !wait_or_abort<true>(&tempty[1], want, a, DEV_TIMEOUT_MMA_TEMPTY, abort_flag, peer_abort)) break;
+                    if (!ok || !wait(std::true_type{}, &tempty[1], want, DEV_TIMEOUT_MMA_TEMPTY)) break;
                     tc_fence_after();
                     uint32_t st = s0;
                     for (int b = 0; b < kb; ++b) {
                         multiply(idesc, st, 1, 1, kBK / 16, b == 0);
-                        commit_pair(&empty[st]);
+                        commit_pair(one, &empty[st]);
                         if (++st == kStages) st = 0;
                     }
                 }
@@ -777,20 +816,22 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                     }
                     multiply(idesc, s, 0, buf0, steps, kb == 0);
                     if (SUB == 2 && subs == 2) {
-                        if (kb == t.kb - 1) commit_pair(&tfull[0]);  // its epilogue runs under the last MMAs
+                        if (kb == t.kb - 1) commit_pair(one, &tfull[0]);  // its epilogue runs under the last MMAs
                         multiply(idesc, s, 1, 1, steps, kb == 0);
                     }
-                    commit_pair(&empty[s]);
+                    commit_pair(one, &empty[s]);
                     if (++s == kStages) { s = 0; ph ^= 1u; }
                 }
-                if (ok) commit_pair(&tfull[SUB == 2 && subs == 2 ? 1 : buf0]);
+                if (ok) commit_pair(one, &tfull[SUB == 2 && subs == 2 ? 1 : buf0]);
                 ++it;
                 uses1 += subs == 2 ? 1u : 0u;
             }
             // every MMA issued is complete before TMEM is freed
-            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                         ::"r"(smem_u32(drain)) : "memory");
-            mbar_drain(drain, 0, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
+            if (one) {  // the thread that issued them
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                             ::"r"(smem_u32(drain)) : "memory");
+                mbar_drain(drain, 0, a.status, DEV_TIMEOUT_DRAIN, a.wait_limit);
+            }
         }
         __syncwarp();
     } else if (WG && warp == kClearWarp) {
