@@ -156,7 +156,10 @@ route_backward_kernel(const float* __restrict__ logits, const int32_t* __restric
 // in flight: blocks of 64 tokens x 128 columns, several to an SM, multiply
 // with warp-level MMAs (16 x 8 x 16; each warp 64 tokens x 16 columns) from a
 // double buffer of 64-term chunks, turn the sums round in shared memory and
-// then walk rows, 16 lanes reading 256 consecutive bytes.  (The same sum in the
+// then walk rows, 16 lanes reading 256 consecutive bytes.  Neighbouring blocks
+// take one strip of columns after the other of the same tokens, so that a row's
+// pieces are read at about the same time (T = 16384, d = 4096, E = 8, K = 2:
+// 89 us, 94 with a strip's tokens in a row).  (The same sum in the
 // epilogue of the CTA-pair GEMM, whose 8 epilogue warps an SM are too few to
 // cover the rows' latency, took 224 us at T = 16384, d = 4096, K = 2.)
 constexpr int kDxTokens = 64, kDxCols = 128, kDxK = 64;
@@ -203,8 +206,9 @@ router_dx_kernel(const bf16* __restrict__ dl, const bf16* __restrict__ Wr, int l
     bf16* const operands = reinterpret_cast<bf16*>(smem);
     float* const out = reinterpret_cast<float*>(smem);  // after the product
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kDxTokens;
-    const int n0 = blockIdx.y * kDxCols;
+    const unsigned strips = (static_cast<unsigned>(d) + kDxCols - 1) / kDxCols;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x / strips) * kDxTokens;
+    const int n0 = static_cast<int>(blockIdx.x % strips) * kDxCols;
     // a chunk's 16-byte units of a row, whole MMA steps
     auto units = [&](int k0) { return min(kDxK, (ld - k0 + 15) / 16 * 16) / 8; };
     stage_dx(operands, dl, Wr, ld, 0, units(0), t0, T, n0, d);
@@ -348,7 +352,7 @@ int launch_route_backward(const float* logits, const int32_t* idx, const float* 
 
 int launch_router_dx(const bf16* dl, const bf16* Wr, int ld, const bf16* dx_perm, const int32_t* inv, int64_t T, int d, int K,
                      void* dx, bool dx_bf16, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>((T + kDxTokens - 1) / kDxTokens), static_cast<unsigned>((d + kDxCols - 1) / kDxCols));
+    const unsigned grid = static_cast<unsigned>((T + kDxTokens - 1) / kDxTokens * ((d + kDxCols - 1) / kDxCols));
     static std::atomic<unsigned long long> done16{0}, done32{0};
     if (dx_bf16) {
         if (smem_attr_once(reinterpret_cast<const void*>(router_dx_kernel<bf16>), dx_smem(256), done16) != 0) return -3;
