@@ -508,6 +508,13 @@ MOE_API int moe_ffn_backward(const moe_dims* dims, const moe_bf16* dy_perm, cons
                              moe_bf16* dgu, moe_bf16* dx_perm, void* dW1, void* dW3, void* dW2, int dw_is_bf16, void* ws,
                              size_t ws_bytes, void* stream);
 
+/* Tile that a product of these two calls takes at these dims: 1 (256 columns)
+ * or 2 (two such sub-tiles, one load of the left operand).  product: 0 G and
+ * U (128 columns of each), 1 Y; 2 dG and dU, 3 dX, 4 dW1, dW3 and dW2 wanted
+ * together.  Results do not depend on it.  Host only (at most a query of the
+ * current device's SM count); MOE_EINVAL on bad dims or another product. */
+MOE_API int moe_train_subtiles(const moe_dims* dims, int product);
+
 /* Gradient of moe_combine: for each kept slot with r = inv[t,k]
  *   dy_perm[r] = topk_w[t,k] * dy[t],  dtopk_w[t,k] = <dy[t], y_perm[r]>.
  *   dy        [T, d_model]: bf16 with dy_is_bf16 != 0, else fp32

@@ -38,7 +38,7 @@ EXPORTED = [
     "moe_test_set_wait_limits", "moe_ep_regroup", "moe_int4_bytes", "moe_int4_pack", "moe_int4_unpack",
     "moe_expert_ffn_slots", "moe_layernorm", "moe_layernorm_workspace_size", "moe_layernorm_backward",
     "moe_ffn_train", "moe_ffn_backward", "moe_combine_backward", "moe_permute_backward",
-    "moe_route_backward_workspace_size", "moe_route_backward",
+    "moe_route_backward_workspace_size", "moe_route_backward", "moe_train_subtiles",
 ]
 LAYERNORM_MAX_WIDTH = 16384
 STATUS_BYTES = 256  # workspace of moe_ffn_train and moe_ffn_backward
@@ -112,6 +112,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_layernorm_backward": (I, [I64, I, P, P, I, P, I, P, P, P, P, P, P, P, SZ, P]),
         "moe_ffn_train": (I, [dims_p, P, P, P, P, P, P, P, P, P, SZ, P]),
         "moe_ffn_backward": (I, [dims_p, P, P, P, P, P, P, P, P, P, P, P, P, P, I, P, SZ, P]),
+        "moe_train_subtiles": (I, [dims_p, I]),
         "moe_combine_backward": (I, [dims_p, P, I, P, P, P, P, P, P]),
         "moe_permute_backward": (I, [dims_p, P, P, P, I, P]),
         "moe_route_backward_workspace_size": (I, [dims_p, ctypes.POINTER(SZ)]),
@@ -536,6 +537,17 @@ def moe_ffn_backward(dims, dy_perm, x_perm, offsets, W1, W3, W2, gu, h, dgu, dx_
         _need(W2, n, BF16, dev, "W2"), _need(gu, 2 * A * f, BF16, dev, "gu"), _may(h, A * f, BF16, dev, "h"),
         _need(dgu, 2 * A * f, BF16, dev, "dgu"), _may(dx_perm, A * d, BF16, dev, "dx_perm"), _may(dW1, n, wt, dev, "dW1"),
         _may(dW3, n, wt, dev, "dW3"), _may(dW2, n, wt, dev, "dW2"), wt is BF16, _need(ws, 0, torch.uint8, dev, "ws"), ws.numel()))
+
+
+TRAIN_PRODUCTS = ("gate", "down", "dgate", "dx", "dw")
+
+
+def moe_train_subtiles(dims, product: str) -> int:
+    """256-column sub-tiles, 1 or 2, of a tile of one of TRAIN_PRODUCTS (see the header)."""
+    n = load().moe_train_subtiles(ctypes.byref(_dims(dims)), TRAIN_PRODUCTS.index(product))
+    if n < 0:
+        _check("moe_train_subtiles", n)
+    return n
 
 
 def moe_combine_backward(dims, dy, y_perm, inv, topk_w, dy_perm, dtopk_w=None, stream=None):

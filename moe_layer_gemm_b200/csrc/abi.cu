@@ -30,7 +30,7 @@ WaitSettings wait_settings() {
 
 namespace {
 
-constexpr int kVersion = 210;  // 2.10: the training entry points.  2.00: y_is_bf16 in moe_combine and both layer calls; MOE_EINDEX;
+constexpr int kVersion = 211;  // 2.11: moe_train_subtiles.  2.10: the training entry points.  2.00: y_is_bf16 in moe_combine and both layer calls; MOE_EINDEX;
                                 // moe_test_set_wait_limits.  1.01: P_topk, aux_topk, z_loss; chunked layer
 // C = ceil(cf * T * K / E) on the exact binary value of cf; -1 = no limit.
 int64_t capacity_of(const moe_dims* d) {

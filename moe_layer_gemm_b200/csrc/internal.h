@@ -244,6 +244,8 @@ struct WeightGradient {
 };
 int launch_train_dw(const WeightGradient* w, int n, const int32_t* off, int64_t chunk, int64_t rows, int G, bool out_bf16,
                     int* status, cudaStream_t st);
+// 256-column sub-tiles of a tile, 1 or 2: gate, down, dgate, dx, all three weight gradients.
+int train_subtiles(int product, int64_t rows, int E, int d, int f);
 
 // ------------------------------------------------------------ training: around the experts (train.cu)
 int launch_combine_backward(const void* dy, bool dy_bf16, const float* y_perm, const int32_t* inv, const float* w, int64_t T,

@@ -146,6 +146,12 @@ int moe_ffn_backward(const moe_dims* dims, const moe_bf16* dy_perm, const moe_bf
     return MOE_OK;
 }
 
+int moe_train_subtiles(const moe_dims* dims, int product) {
+    MOE_TRY(check_dims(dims));
+    if (product < 0 || product > 4) return MOE_EINVAL;
+    return train_subtiles(product, dims->T * dims->K, dims->E, dims->d_model, dims->d_ff);
+}
+
 int moe_combine_backward(const moe_dims* dims, const void* dy, int dy_is_bf16, const float* y_perm, const int32_t* inv,
                          const float* topk_w, moe_bf16* dy_perm, float* dtopk_w, void* stream) {
     MOE_TRY(check_dims(dims));

@@ -1050,33 +1050,42 @@ int launch_sub(const Maps& maps, Args a, int64_t max_tiles, cudaStream_t st) {
 }
 
 // K-blocks of a tile from which it takes two sub-tiles.  The epilogue that the
-// next tile then waits for has to be a small part of it; it is longest where
-// it reads the saved projections too, and longer with three outputs.  Two
-// sub-tiles against one, ms: down (224 k-blocks) 2.88, 3.26; dx (448) 5.30,
-// 6.40, (44) 0.299, 0.312; weight gradients (64) 6.65, 8.33, (7) 0.47, 0.44;
-// gate (64) 6.46, 6.68; dgate (64) 4.01, 3.63, (32) 0.263, 0.204.
-constexpr int wide_from(int epi) { return epi == E_DGATE ? 128 : (epi == E_GATE ? 64 : 32); }
+// next tile then waits for has to be a small part of it; it is longer with
+// three outputs.  Two sub-tiles against one, ms: down (224 k-blocks) 2.88,
+// 3.26; dx (448) 5.30, 6.40, (44) 0.299, 0.312; weight gradients (64) 6.65,
+// 8.33, (7) 0.47, 0.44; gate (64) 6.46, 6.68.  The saved projections' gradient
+// always takes one: its epilogue reads them too, and with two sub-tiles it
+// measured from 0.92 to 1.09 times as fast at 128 to 512 k-blocks, slower below.
+constexpr int kNever = 1 << 30;
+constexpr int wide_from(int epi) { return epi == E_DGATE ? kNever : (epi == E_GATE ? 64 : 32); }
+constexpr int sub_cols(int epi) { return epi == E_GATE ? 128 : 256; }
 
-// `kb`: k-blocks of a tile (of an average one, for weight gradients); `row_tiles`:
-// token-major: an upper bound of all groups' row tiles.
+// Sub-tiles of a tile of `kb` k-blocks (of an average one, for weight gradients).
+int sub_tiles(int epi, const Args& a, int kb) {
+    int widest = 0;
+    for (int j = 0; j < a.products; ++j) widest = a.p[j].N > widest ? a.p[j].N : widest;
+    return kb >= wide_from(epi) && widest > sub_cols(epi) ? 2 : 1;
+}
+
+// `kb`: see sub_tiles; `row_tiles`: token-major: an upper bound of all groups' row tiles.
 template <int EPI, bool B_MN>
 int launch(const Maps& maps, Args a, int kb, int64_t row_tiles, cudaStream_t st) {
     if (a.G < 1 || a.G > kMaxGroups) return -2;
     const WaitSettings wt = wait_settings();
     a.wait_limit = wt.wait_limit ? wt.wait_limit : kWaitLimit;
     a.never_ready = wt.dep_never_ready;
-    const int sub_cols = EPI == E_GATE ? 128 : 256;
-    int widest = 0;
-    for (int j = 0; j < a.products; ++j) widest = a.p[j].N > widest ? a.p[j].N : widest;
-    const int sub = kb >= wide_from(EPI) && widest > sub_cols ? 2 : 1;
+    const int sub = sub_tiles(EPI, a, kb);
     for (int j = 0; j < a.products; ++j) {
         Product& p = a.p[j];
-        p.n_tiles = ceil_div(p.N, sub * sub_cols);
+        p.n_tiles = ceil_div(p.N, sub * sub_cols(EPI));
         p.m_tiles = ceil_div(p.M, 256);
         a.group_tiles += p.m_tiles * p.n_tiles;
     }
     const int64_t tiles = EPI == E_WGRAD ? static_cast<int64_t>(a.G) * a.group_tiles : row_tiles * a.p[0].n_tiles;
-    return sub == 2 ? launch_sub<EPI, B_MN, 2>(maps, a, tiles, st) : launch_sub<EPI, B_MN, 1>(maps, a, tiles, st);
+    if constexpr (wide_from(EPI) != kNever) {
+        if (sub == 2) return launch_sub<EPI, B_MN, 2>(maps, a, tiles, st);
+    }
+    return launch_sub<EPI, B_MN, 1>(maps, a, tiles, st);
 }
 
 // What the token-major products share.
@@ -1178,6 +1187,19 @@ int launch_train_dw(const WeightGradient* w, int n, const int32_t* off, int64_t 
     a.out_bf16 = out_bf16 ? 1 : 0;
     a.status = status;
     return launch<E_WGRAD, true>(m, a, ceil_div(off ? rows / G : chunk, kBK), 0, st);
+}
+
+int train_subtiles(int product, int64_t rows, int E, int d, int f) {
+    const bool narrow_out = product == E_F32 || product == E_BF16;  // width d, reduction over f
+    const int k = ceil_div(narrow_out ? f : d, kBK) * (product == E_BF16 ? 2 : 1);
+    Args a = token_major(nullptr, rows, E, narrow_out ? d : f, 0, nullptr, k, k, nullptr);
+    if (product == E_WGRAD) {
+        a.products = kProducts;
+        a.p[0].M = a.p[1].M = a.p[2].N = d;
+        a.p[2].M = a.p[0].N = a.p[1].N = f;
+        a.kb_all = ceil_div(rows / E, kBK);
+    }
+    return sub_tiles(product, a, a.kb_all);
 }
 
 }  // namespace moe
