@@ -1026,13 +1026,11 @@ constexpr size_t smem_of(int epi) {
 static_assert(smem_of(E_GATE) <= 232448 && smem_of(E_DGATE) <= 232448 && smem_of(E_WGRAD) <= 232448, "227 KB a CTA");
 
 template <int EPI, bool B_MN, int SUB>
-int launch_sub(const Maps& maps, Args a, int64_t max_tiles, cudaStream_t st) {
+int launch_sub(const Maps& maps, const Args& a, int pairs, int64_t max_tiles, cudaStream_t st) {
     static std::atomic<unsigned long long> attr_done{0};
     const auto kernel = train_gemm_kernel<EPI, B_MN, SUB>;
     constexpr size_t kSmem = smem_of(EPI);
     if (smem_attr_once(reinterpret_cast<const void*>(kernel), static_cast<int>(kSmem), attr_done) != 0) return -3;
-    int pairs = num_sms() / 2;
-    if (pairs < 1) return -3;
     if (pairs > max_tiles) pairs = static_cast<int>(max_tiles);
     // Programmatic launch: where the tiles are few, the set-up of one product's
     // kernel runs on free SMs under the previous product's end.
@@ -1060,32 +1058,58 @@ constexpr int kNever = 1 << 30;
 constexpr int wide_from(int epi) { return epi == E_DGATE ? kNever : (epi == E_GATE ? 64 : 32); }
 constexpr int sub_cols(int epi) { return epi == E_GATE ? 128 : 256; }
 
-// Sub-tiles of a tile of `kb` k-blocks (of an average one, for weight gradients).
-int sub_tiles(int epi, const Args& a, int kb) {
-    int widest = 0;
-    for (int j = 0; j < a.products; ++j) widest = a.p[j].N > widest ? a.p[j].N : widest;
-    return kb >= wide_from(epi) && widest > sub_cols(epi) ? 2 : 1;
+// Tiles of a launch whose tiles have `sub` sub-tiles, laid out in `a`; a
+// token-major one has `row_tiles` row tiles.
+int64_t lay_out(Args& a, int epi, int sub, int64_t row_tiles) {
+    a.group_tiles = 0;
+    for (int j = 0; j < a.products; ++j) {
+        Product& p = a.p[j];
+        p.n_tiles = ceil_div(p.N, sub * sub_cols(epi));
+        p.m_tiles = ceil_div(p.M, 256);
+        a.group_tiles += p.m_tiles * p.n_tiles;
+    }
+    return epi == E_WGRAD ? static_cast<int64_t>(a.G) * a.group_tiles : row_tiles * a.p[0].n_tiles;
 }
 
-// `kb`: see sub_tiles; `row_tiles`: token-major: an upper bound of all groups' row tiles.
+// Sub-tiles of a tile of `kb` k-blocks (of an average one, for weight
+// gradients).  Two need a long reduction and tiles enough for every pair: the
+// pairs take their tiles in rounds, and a round of wide tiles costs about 0.92
+// of two narrow ones (0.83 to 0.96 in the figures above), so the wide tiles'
+// rounds must be few enough.  Few tiles of two sub-tiles leave pairs idle.
+// One sub-tile against two, us, with the rounds of each:
+//   down  f = 14336, 256 rows, d = 4096        (1, 1)   104, 190
+//         f = 4096, d = 1024, 10240 rows       (3, 2)    87, 109; 19456 rows (5, 3) 157, 174
+//         f = 4096, d = 2048, 7168 rows        (4, 2)   117, 119
+//   dx    f = 4096, d = 4096, 4096 rows        (4, 2)   199, 192
+//         f = 2048, d = 8192 / 16384, 4096 rows (7, 4)  175, 197; (14, 7) 368, 358
+//   dw    d = f = 1024, 8192 rows              (1, 1)    62, 124; d = f = 4096 (11, 6) 543, 604
+// The row tiles are not known here: a group's last one is taken to be half full.
+int sub_tiles(int epi, Args a, int kb, int pairs) {
+    int widest = 0;
+    for (int j = 0; j < a.products; ++j) widest = a.p[j].N > widest ? a.p[j].N : widest;
+    if (kb < wide_from(epi) || widest <= sub_cols(epi)) return 1;
+    const int64_t groups = a.G < a.cap ? a.G : a.cap, likely = (a.cap + 255) / 256 + a.G / 2;
+    const int64_t row_tiles = likely > groups ? likely : groups;
+    const int64_t one = (lay_out(a, epi, 1, row_tiles) + pairs - 1) / pairs, two = (lay_out(a, epi, 2, row_tiles) + pairs - 1) / pairs;
+    return 92 * 2 * two <= 100 * one ? 2 : 1;
+}
+
+// `kb`: see sub_tiles.
 template <int EPI, bool B_MN>
-int launch(const Maps& maps, Args a, int kb, int64_t row_tiles, cudaStream_t st) {
+int launch(const Maps& maps, Args a, int kb, cudaStream_t st) {
     if (a.G < 1 || a.G > kMaxGroups) return -2;
     const WaitSettings wt = wait_settings();
     a.wait_limit = wt.wait_limit ? wt.wait_limit : kWaitLimit;
     a.never_ready = wt.dep_never_ready;
-    const int sub = sub_tiles(EPI, a, kb);
-    for (int j = 0; j < a.products; ++j) {
-        Product& p = a.p[j];
-        p.n_tiles = ceil_div(p.N, sub * sub_cols(EPI));
-        p.m_tiles = ceil_div(p.M, 256);
-        a.group_tiles += p.m_tiles * p.n_tiles;
-    }
-    const int64_t tiles = EPI == E_WGRAD ? static_cast<int64_t>(a.G) * a.group_tiles : row_tiles * a.p[0].n_tiles;
+    const int pairs = num_sms() / 2;
+    if (pairs < 1) return -3;
+    const int sub = sub_tiles(EPI, a, kb, pairs);
+    // at most this many row tiles: every group's last one may be partial
+    const int64_t tiles = lay_out(a, EPI, sub, (a.cap + 255) / 256 + a.G);
     if constexpr (wide_from(EPI) != kNever) {
-        if (sub == 2) return launch_sub<EPI, B_MN, 2>(maps, a, tiles, st);
+        if (sub == 2) return launch_sub<EPI, B_MN, 2>(maps, a, pairs, tiles, st);
     }
-    return launch_sub<EPI, B_MN, 1>(maps, a, tiles, st);
+    return launch_sub<EPI, B_MN, 1>(maps, a, pairs, tiles, st);
 }
 
 // What the token-major products share.
@@ -1104,9 +1128,6 @@ Args token_major(const int32_t* off, int64_t rows, int E, int N, int64_t ld, voi
     return a;
 }
 
-// Upper bound of a token-major launch's row tiles: a group's last one may be partial.
-int64_t row_tile_bound(int64_t rows, int G) { return (rows + 255) / 256 + G; }
-
 }  // namespace
 
 int launch_train_gate(const bf16* x, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W1,
@@ -1120,7 +1141,7 @@ int launch_train_gate(const bf16* x, const int32_t* off, int64_t rows, int E, in
     m.ah[1] = m.ah[0];
     Args a = token_major(off, rows, E, f, 2 * static_cast<int64_t>(f), gu, ceil_div(d, kBK), ceil_div(d, kBK), status);
     a.h = h;
-    return launch<E_GATE, true>(m, a, a.kb_all, row_tile_bound(rows, E), st);
+    return launch<E_GATE, true>(m, a, a.kb_all, st);
 }
 
 int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2, float* y,
@@ -1132,7 +1153,7 @@ int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, in
     m.ah[1] = m.ah[0];
     m.b[1] = m.b[0];
     Args a = token_major(off, rows, E, d, d, y, ceil_div(f, kBK), ceil_div(f, kBK), status);
-    return launch<E_F32, true>(m, a, a.kb_all, row_tile_bound(rows, E), st);
+    return launch<E_F32, true>(m, a, a.kb_all, st);
 }
 
 int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2,
@@ -1148,7 +1169,7 @@ int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, 
     m.b[1] = m.b[0];
     Args a = token_major(off, rows, E, f, 2 * static_cast<int64_t>(f), dgu, ceil_div(d, kBK), ceil_div(d, kBK), status);
     a.gu = gu;
-    return launch<E_DGATE, false>(m, a, a.kb_all, row_tile_bound(rows, E), st);
+    return launch<E_DGATE, false>(m, a, a.kb_all, st);
 }
 
 int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W1,
@@ -1161,7 +1182,7 @@ int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, in
         !map_weights(&m.b[0], W1, E, d, f, 128) || !map_weights(&m.b[1], W3, E, d, f, 128))
         return -3;
     Args a = token_major(off, rows, E, d, d, dx, ceil_div(f, kBK), 2 * ceil_div(f, kBK), status);
-    return launch<E_BF16, false>(m, a, a.kb_all, row_tile_bound(rows, E), st);
+    return launch<E_BF16, false>(m, a, a.kb_all, st);
 }
 
 int launch_train_dw(const WeightGradient* w, int n, const int32_t* off, int64_t chunk, int64_t rows, int G, bool out_bf16,
@@ -1186,7 +1207,7 @@ int launch_train_dw(const WeightGradient* w, int n, const int32_t* off, int64_t 
     a.G = G;
     a.out_bf16 = out_bf16 ? 1 : 0;
     a.status = status;
-    return launch<E_WGRAD, true>(m, a, ceil_div(off ? rows / G : chunk, kBK), 0, st);
+    return launch<E_WGRAD, true>(m, a, ceil_div(off ? rows / G : chunk, kBK), st);
 }
 
 int train_subtiles(int product, int64_t rows, int E, int d, int f) {
@@ -1199,7 +1220,7 @@ int train_subtiles(int product, int64_t rows, int E, int d, int f) {
         a.p[2].M = a.p[0].N = a.p[1].N = f;
         a.kb_all = ceil_div(rows / E, kBK);
     }
-    return sub_tiles(product, a, a.kb_all);
+    return sub_tiles(product, a, a.kb_all, (num_sms() > 0 ? num_sms() : 148) / 2);
 }
 
 }  // namespace moe

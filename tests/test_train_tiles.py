@@ -28,6 +28,17 @@ def test_saved_projections_gradient_takes_narrow_tiles(T, d, f, E, K):
     assert tiles("dgate", T, d, f, E, K) == 1
 
 
+@pytest.mark.parametrize("product,T,d,f,E,K,want", [
+    # 16 narrow tiles on 74 pairs, or 8 wide ones that take twice as long
+    ("down", 256, 4096, 14336, 1, 1, 1), ("dx", 256, 4096, 14336, 1, 1, 1), ("down", 128, 2048, 8192, 7, 2, 1), ("dw", 8192, 1024, 1024, 1, 1, 1),
+    # rounds of narrow and wide tiles: (3, 2), (5, 3), (7, 4) and, for all three weight gradients, (11, 6)
+    ("down", 10240, 1024, 4096, 1, 1, 1), ("down", 19456, 1024, 4096, 1, 1, 1), ("dx", 4096, 8192, 2048, 1, 1, 1), ("dw", 8192, 4096, 4096, 1, 1, 1),
+    # (4, 2), (14, 7) and more: wide
+    ("down", 7168, 2048, 4096, 1, 1, 2), ("dx", 4096, 16384, 2048, 1, 1, 2), ("gate", 256, 4096, 14336, 8, 2, 2), ("dx", 8192, 2048, 1408, 60, 4, 2)])
+def test_few_tiles_are_not_halved(product, T, d, f, E, K, want):
+    assert tiles(product, T, d, f, E, K) == want
+
+
 def test_refusals():
     with pytest.raises(abi.MoEError):
         tiles("gate", 0, 128, 128)
