@@ -102,8 +102,8 @@ MOE_API int moe_version(void);
  * launch ends early, with MOE_ETIMEOUT and detail 6 in the workspace status
  * flag, after its abort and drain paths have run; its outputs are undefined.
  * The products of the training calls take wait_polls too; there, with
- * dependency_never_ready != 0, the epilogues wait for an event that never
- * comes (MOE_ETIMEOUT, detail 4).
+ * dependency_never_ready != 0, it limits the epilogues' waits alone, which
+ * are for an event that never comes (MOE_ETIMEOUT, detail 4).
  * Lets a test exercise those paths without faulting or hanging anything.
  * Process-wide and not synchronised with launches in flight on other
  * threads: call it only between launches. */

@@ -103,7 +103,11 @@ struct Args {
     int out_bf16;          // E_WGRAD: bf16 output, else fp32
     int* status;
     uint32_t wait_limit;
-    int never_ready;  // a test of the timeout paths: the epilogue waits for what nothing completes
+    // A test of the timeout paths: the epilogue waits, `epi_limit` polls, for what
+    // nothing completes.  The other waits keep the default limit, so that theirs
+    // cannot run out first, which polls faster or slower than the epilogue's.
+    int never_ready;
+    uint32_t epi_limit;
 };
 
 struct Maps {
@@ -275,12 +279,12 @@ __device__ __forceinline__ float sigmoid(float x) {
     return r;
 }
 
-// A wait that gives up after a.wait_limit polls; its failure, or an abort
-// seen, stops both CTAs of the pair.
+// A wait that gives up after `limit` polls; its failure, or an abort seen, stops
+// both CTAs of the pair.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const Args& a, int code,
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const Args& a, uint32_t limit, int code,
                                               volatile int* abort_flag, uint32_t peer_abort) {
-    for (uint32_t i = 0; i < a.wait_limit; ++i) {
+    for (uint32_t i = 0; i < limit; ++i) {
         if (CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if ((i & 255u) == 255u) {
             if (*abort_flag) return false;
@@ -295,9 +299,9 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, co
 
 // The same for a whole warp: every lane leaves with the same answer.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Args& a, int code,
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Args& a, uint32_t limit, int code,
                                           volatile int* abort_flag, uint32_t peer_abort) {
-    return __all_sync(0xffffffffu, wait_or_abort<CLUSTER>(bar, parity, a, code, abort_flag, peer_abort)) != 0;
+    return __all_sync(0xffffffffu, wait_or_abort<CLUSTER>(bar, parity, a, limit, code, abort_flag, peer_abort)) != 0;
 }
 
 // An accumulator has a row per lane; stored from there, one instruction would
@@ -664,7 +668,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             const int n0 = col0 + (EPI == E_GATE ? 64 : 128) * static_cast<int>(rank);
             const uint32_t bytes = static_cast<uint32_t>(subs) * kOperand + (half ? kOperand / 2 : kOperand);
             for (int kb = 0; kb < t.kb; ++kb) {
-                if (!warp_wait(&empty[s], ph ^ 1u, a, DEV_TIMEOUT_PRODUCER_EMPTY, abort_flag, peer_abort)) {
+                if (!warp_wait(&empty[s], ph ^ 1u, a, a.wait_limit, DEV_TIMEOUT_PRODUCER_EMPTY, abort_flag, peer_abort)) {
                     ok = false;
                     break;
                 }
@@ -736,8 +740,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             const uint32_t one = kWarp ? elect_one() : 1u;
             auto wait = [&](auto cluster, uint64_t* bar, uint32_t parity, int code) -> bool {
                 constexpr bool kCluster = decltype(cluster)::value;
-                if (kWarp) return warp_wait<kCluster>(bar, parity, a, code, abort_flag, peer_abort);
-                return wait_or_abort<kCluster>(bar, parity, a, code, abort_flag, peer_abort);
+                if (kWarp) return warp_wait<kCluster>(bar, parity, a, a.wait_limit, code, abort_flag, peer_abort);
+                return wait_or_abort<kCluster>(bar, parity, a, a.wait_limit, code, abort_flag, peer_abort);
             };
             auto same = [&](int v) { return kWarp ? uniform(v) : v; };
             // idesc: D fp32, A and B bf16, bits 15 and 16 set where A, B are M-, N-contiguous
@@ -848,7 +852,7 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             const uint32_t st = (s + kStages - 1) % kStages;
             const uint32_t tph = (tail_ph >> st) & 1u;
             tail_ph ^= 1u << st;
-            if (!warp_wait(&tail[st], tph, a, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) break;
+            if (!warp_wait(&tail[st], tph, a, a.wait_limit, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) break;
             const int subs = SUB == 1 ? 1 : min(SUB, (a.p[t.j].N - t.n * SUB * kSubCols + kSubCols - 1) / kSubCols);
             const int from = t.k_tail * 8, to = (t.k_tail + 15) / 16 * 128;  // 16-byte units of a 64-column box
             uint4* box = reinterpret_cast<uint4*>(smem + st * kStageBytes);
@@ -892,8 +896,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                 const uint32_t use = SUB == 1 ? static_cast<uint32_t>(it >> 1) : (j ? uses1 : static_cast<uint32_t>(it));
                 const bool mine = rows > 0 && col0 < p.N;
                 if (mine && !WG) epi.load(p, row0, rows, col0);
-                if (!warp_wait(a.never_ready ? never : &tfull[buf], a.never_ready ? 0u : use & 1u, a, DEV_TIMEOUT_EPI_TFULL, abort_flag,
-                               peer_abort)) {
+                if (!warp_wait(a.never_ready ? never : &tfull[buf], a.never_ready ? 0u : use & 1u, a, a.epi_limit, DEV_TIMEOUT_EPI_TFULL,
+                               abort_flag, peer_abort)) {
                     ok = false;
                     break;
                 }
@@ -1099,8 +1103,9 @@ template <int EPI, bool B_MN>
 int launch(const Maps& maps, Args a, int kb, cudaStream_t st) {
     if (a.G < 1 || a.G > kMaxGroups) return -2;
     const WaitSettings wt = wait_settings();
-    a.wait_limit = wt.wait_limit ? wt.wait_limit : kWaitLimit;
+    a.epi_limit = wt.wait_limit ? wt.wait_limit : kWaitLimit;
     a.never_ready = wt.dep_never_ready;
+    a.wait_limit = a.never_ready ? kWaitLimit : a.epi_limit;
     const int pairs = num_sms() / 2;
     if (pairs < 1) return -3;
     const int sub = sub_tiles(EPI, a, kb, pairs);

@@ -6,9 +6,12 @@ side.  Widths leave a last tile of one sub-tile.  Bounds as in the tests of
 the same calls at other sizes: half a step of the output's type and one fp32
 step of the sum of magnitudes a term.
 """
+import time
+
 import pytest
 import torch
 from test_gpu_train import BF16, F32, F64, I32, MARK, STEP, behind_is_nan, check, gen, marked, normal, status_ok
+from test_gpu_train_step import Step, _bits
 
 from moe_layer_gemm_b200 import abi
 
@@ -88,3 +91,30 @@ def test_backward(A, d, f, sizes, wide, dw):
         check(dW3[e], xe.T @ dU, m * STEP * (xe.T.abs() @ dU.abs()), f"dW3 of {e}")
         check(dW2[e], hk.T @ dye, m * STEP * (hk.T.abs() @ dye.abs()), f"dW2 of {e}")
     assert (dgu[n:] == MARK).all() and (dx[n:] == MARK).all()
+
+
+def test_timeouts_of_wide_tiles_end_and_leave_the_context_usable():
+    """As for narrow tiles: every epilogue waits for what never comes, in the middle of many tiles."""
+    s = Step(7500, 4304, 4304, 2, 1, seed=6)
+    assert [abi.moe_train_subtiles(s.dims, p) for p in ("gate", "down", "dx", "dw")] == [2, 2, 2, 2]
+    s.run()
+    want = _bits(s.results())
+    torch.cuda.synchronize()
+    try:
+        abi.moe_test_set_wait_limits(1 << 14, 0, True)
+        t0 = time.perf_counter()
+        abi.moe_ffn_train(s.dims, s.x_perm, s.offsets, s.W1, s.W3, s.W2, s.gu, s.h, s.y_perm, s.tws)
+        torch.cuda.synchronize()
+        assert abi.moe_get_device_status(s.tws) == (abi.MOE_ETIMEOUT, 4)
+        abi.moe_reset_device_status(s.tws)
+        abi.moe_ffn_backward(s.dims, s.dy_perm, s.x_perm, s.offsets, s.W1, s.W3, s.W2, s.gu, s.h, s.dgu, s.dx_perm, s.grads["W1"],
+                             s.grads["W3"], s.grads["W2"], s.tws)
+        torch.cuda.synchronize()
+        assert abi.moe_get_device_status(s.tws) == (abi.MOE_ETIMEOUT, 4)
+        assert time.perf_counter() - t0 < 10.0
+    finally:
+        abi.moe_test_set_wait_limits(0, 0, False)
+    abi.moe_reset_device_status(s.tws)
+    s.run()
+    assert abi.moe_get_device_status(s.tws) == (abi.MOE_OK, 0)
+    assert all(torch.equal(a, b) for a, b in zip(_bits(s.results()), want))
