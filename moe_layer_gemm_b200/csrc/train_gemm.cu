@@ -269,10 +269,12 @@ __device__ __forceinline__ void unpack8(const uint4& q, float* v) {
     v[4] = bf_lo(q.z), v[5] = bf_hi(q.z), v[6] = bf_lo(q.w), v[7] = bf_hi(q.w);
 }
 
-// Logistic function with the approximate reciprocal and exponential: what
-// comes of it is rounded to bf16, whose step is 2^14 times their error.  For x
-// below -88 the exponential overflows to infinity, whose reciprocal is 0, the
-// limit.
+// Logistic function with the approximate reciprocal and exponential.  The
+// exponential's documented error, 2 + 1.173 |x| units in the last place, is
+// that of the result where x is far below 0: 2^-21 of the value at x = -1,
+// 2^-18 at -20, 2^-16 at -87.  What comes of it is rounded to bf16, by up to
+// 2^-8 of the value.  Below 2^-126 (x < -87.3) the reciprocal flushes to 0,
+// as it does where the exponential overflows (x < -88.7).
 __device__ __forceinline__ float sigmoid(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
