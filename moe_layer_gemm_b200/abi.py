@@ -163,9 +163,23 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name: str = "") -> Optional[int]
     return t.data_ptr()
 
 
+def _current_device() -> int:
+    try:  # torch.cuda.current_device() without its check for a first use: every tensor is on a device by now
+        return torch._C._cuda_getDevice()
+    except AttributeError:
+        return torch.cuda.current_device()
+
+
+def _current_stream(dev: int) -> int:
+    try:  # torch.cuda.current_stream() takes 3 us
+        return torch._C._cuda_getCurrentRawStream(dev)
+    except AttributeError:
+        return torch.cuda.current_stream(dev).cuda_stream
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())  # current_stream() takes 3 us
+        return _current_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -467,10 +481,10 @@ def _device_of(t, name: str) -> int:
 
 def _launch(fn, name: str, dev: int, stream, args):
     """Run a library call on device `dev` and, unless told otherwise, its current stream."""
-    if torch._C._cuda_getDevice() != dev:
+    if _current_device() != dev:
         with torch.cuda.device(dev):
             return _launch(fn, name, dev, stream, args)
-    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    st = _current_stream(dev) if stream is None else _stream(stream)
     status = fn(*args, st)
     if status != MOE_OK:
         _check(name, status)
