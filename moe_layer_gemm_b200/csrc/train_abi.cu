@@ -45,7 +45,8 @@ RouteLayout route_layout(const moe_dims* d) {
     const int m_tiles = (d->d_model + 255) / 256;
     const int pairs = (num_sms() > 0 ? num_sms() : 148) / 2;
     // two rounds of tiles for a narrow weight (E = 8, d = 4096: 144 tiles on 74 pairs;
-    // one round of 64 left a seventh of them idle), one where the partial sums are large
+    // one round of 64 left a seventh of them idle), one where the partial sums are large;
+    // at most 16 chunks, so below d = 2304 fewer tiles than that
     int64_t S = (L.ld <= 64 ? 2 * pairs : pairs) / m_tiles;
     const int64_t most = (d->T + 255) / 256;  // at least 256 tokens a chunk
     if (S > most) S = most;
