@@ -510,8 +510,8 @@ MOE_API int moe_ffn_backward(const moe_dims* dims, const moe_bf16* dy_perm, cons
 
 /* Tile that a product of these two calls takes at these dims: 1 (256 columns)
  * or 2 (two such sub-tiles, one load of the left operand).  product: 0 G and
- * U (128 columns of each), 1 Y; 2 dG and dU, 3 dX, 4 dW1, dW3 and dW2 wanted
- * together.  Results do not depend on it.  Host only (at most a query of the
+ * U (128 columns of each), 1 Y; 2 dG and dU, 3 dX, 4 dW1, dW3 and dW2 (2 and
+ * 4 always take one).  Results do not depend on it.  Host only (at most a query of the
  * current device's SM count); MOE_EINVAL on bad dims or another product. */
 MOE_API int moe_train_subtiles(const moe_dims* dims, int product);
 

@@ -244,7 +244,7 @@ struct WeightGradient {
 };
 int launch_train_dw(const WeightGradient* w, int n, const int32_t* off, int64_t chunk, int64_t rows, int G, bool out_bf16,
                     int* status, cudaStream_t st);
-// 256-column sub-tiles of a tile, 1 or 2: gate, down, dgate, dx, all three weight gradients.
+// 256-column sub-tiles of a tile, 1 or 2: gate, down, dgate, dx, weight gradients.
 int train_subtiles(int product, int64_t rows, int E, int d, int f);
 
 // ------------------------------------------------------------ training: around the experts (train.cu)

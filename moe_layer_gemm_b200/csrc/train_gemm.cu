@@ -559,7 +559,7 @@ struct Epilogue {
 // 3/4 of the bytes are loaded; in exchange the next tile waits for the
 // epilogue, except that up to a ring of its k-blocks are multiplied into the
 // first accumulator while the second is still being read.
-template <int EPI, bool B_MN, int SUB>
+template <int EPI, bool B_MN, int SUB>  // weight gradients: SUB = 1
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(EPI == E_WGRAD ? kThreads + 32 : kThreads, 1)
 train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
     constexpr bool WG = EPI == E_WGRAD;
@@ -692,11 +692,8 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
                     const int m0 = t.m * 256 + 128 * static_cast<int>(rank);
                     load_2d(one, &maps.a[t.j], sa, bar, m0, y);
                     load_2d(one, &maps.a[t.j], sa + 8192, bar, m0 + 64, y);
-                    for (int j = 0; j < subs; ++j) {
-                        const uint32_t sb = sa + (1 + j) * kOperand;
-                        load_2d(one, &maps.b[t.j], sb, bar, n0 + 256 * j, y);
-                        load_2d(one, &maps.b[t.j], sb + 8192, bar, n0 + 256 * j + 64, y);
-                    }
+                    load_2d(one, &maps.b[t.j], sa + kOperand, bar, n0, y);
+                    load_2d(one, &maps.b[t.j], sa + kOperand + 8192, bar, n0 + 64, y);
                 } else {
                     const int second = kb >= a.kb_first ? 1 : 0;
                     const int k0 = (kb - (second ? a.kb_first : 0)) * kBK;
@@ -855,11 +852,10 @@ train_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
             const uint32_t tph = (tail_ph >> st) & 1u;
             tail_ph ^= 1u << st;
             if (!warp_wait(&tail[st], tph, a, a.wait_limit, DEV_TIMEOUT_MMA_FULL, abort_flag, peer_abort)) break;
-            const int subs = SUB == 1 ? 1 : min(SUB, (a.p[t.j].N - t.n * SUB * kSubCols + kSubCols - 1) / kSubCols);
             const int from = t.k_tail * 8, to = (t.k_tail + 15) / 16 * 128;  // 16-byte units of a 64-column box
             uint4* box = reinterpret_cast<uint4*>(smem + st * kStageBytes);
             for (int i = from + lane; i < to; i += 32)
-                for (int b = 0; b < 2 + 2 * subs; ++b) box[b * 512 + i] = make_uint4(0u, 0u, 0u, 0u);
+                for (int b = 0; b < 4; ++b) box[b * 512 + i] = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive_cluster(leader_clear + 8u * st);
@@ -1054,14 +1050,17 @@ int launch_sub(const Maps& maps, const Args& a, int pairs, int64_t max_tiles, cu
 }
 
 // K-blocks of a tile from which it takes two sub-tiles.  The epilogue that the
-// next tile then waits for has to be a small part of it; it is longer with
-// three outputs.  Two sub-tiles against one, ms: down (224 k-blocks) 2.88,
-// 3.26; dx (448) 5.30, 6.40, (44) 0.299, 0.312; weight gradients (64) 6.65,
-// 8.33, (7) 0.47, 0.44; gate (64) 6.46, 6.68.  The saved projections' gradient
-// always takes one: its epilogue reads them too, and with two sub-tiles it
-// measured from 0.92 to 1.09 times as fast at 128 to 512 k-blocks, slower below.
+// next tile then waits for has to be a small part of it.  One sub-tile against
+// two, ms, from idle:
+//   gate  64 k-blocks  5.67, 5.58 (Mixtral-shaped batch); 112  1.45, 1.37; 256  1.57, 1.38
+//   down  32  0.83, 0.94; 128  0.89, 0.93; 160  1.11, 1.10 and 1.10, 1.02; 224  2.96, 2.82
+//   dx    44  0.301, 0.314; 64  0.414, 0.405 and 0.430, 0.445; 128  0.84, 0.77; 448  5.77, 5.41
+// The two others always take one.  The saved projections' gradient, whose
+// epilogue reads them too, was from 0.92 to 1.09 times as fast with two at 128
+// to 512 k-blocks and slower below; weight gradients were from 0.92 to 1.03
+// times as fast at 32 to 1024.
 constexpr int kNever = 1 << 30;
-constexpr int wide_from(int epi) { return epi == E_DGATE ? kNever : (epi == E_GATE ? 64 : 32); }
+constexpr int wide_from(int epi) { return epi == E_GATE ? 64 : (epi == E_F32 ? 160 : (epi == E_BF16 ? 128 : kNever)); }
 constexpr int sub_cols(int epi) { return epi == E_GATE ? 128 : 256; }
 
 // Tiles of a launch whose tiles have `sub` sub-tiles, laid out in `a`; a
@@ -1077,32 +1076,27 @@ int64_t lay_out(Args& a, int epi, int sub, int64_t row_tiles) {
     return epi == E_WGRAD ? static_cast<int64_t>(a.G) * a.group_tiles : row_tiles * a.p[0].n_tiles;
 }
 
-// Sub-tiles of a tile of `kb` k-blocks (of an average one, for weight
-// gradients).  Two need a long reduction and tiles enough for every pair: the
-// pairs take their tiles in rounds, and a round of wide tiles costs about 0.92
-// of two narrow ones (0.83 to 0.96 in the figures above), so the wide tiles'
-// rounds must be few enough.  Few tiles of two sub-tiles leave pairs idle.
-// One sub-tile against two, us, with the rounds of each:
-//   down  f = 14336, 256 rows, d = 4096        (1, 1)   104, 190
-//         f = 4096, d = 1024, 10240 rows       (3, 2)    87, 109; 19456 rows (5, 3) 157, 174
-//         f = 4096, d = 2048, 7168 rows        (4, 2)   117, 119
-//   dx    f = 4096, d = 4096, 4096 rows        (4, 2)   199, 192
-//         f = 2048, d = 8192 / 16384, 4096 rows (7, 4)  175, 197; (14, 7) 368, 358
-//   dw    d = f = 1024, 8192 rows              (1, 1)    62, 124; d = f = 4096 (11, 6) 543, 604
+// Sub-tiles of a tile.  Two need a long reduction and tiles enough for every
+// pair: the pairs take their tiles in rounds, and a round of wide tiles costs
+// about 0.92 of two narrow ones (0.88 to 1 in the figures above), so the wide
+// tiles' rounds must be few enough.  Few tiles of two sub-tiles leave pairs
+// idle.  One sub-tile against two, us, with the rounds of each:
+//   down  f = 14336, d = 4096, one group of 256 rows       (1, 1)  104, 190
+//         the same, 8 groups of about 256 / 512 rows       (3, 2)  381, 493; (5, 3) 603, 781
+//   dx    f = 14336, d = 4096, one group of 256 rows       (1, 1)  187, 307
+//         f = 8192, d = 4096, 8 groups of about 256 rows   (3, 2)  296, 369
+//         f = 4096, d = 4096, one group of 4096 rows       (4, 2)  199, 192
 // The row tiles are not known here: a group's last one is taken to be half full.
-int sub_tiles(int epi, Args a, int kb, int pairs) {
-    int widest = 0;
-    for (int j = 0; j < a.products; ++j) widest = a.p[j].N > widest ? a.p[j].N : widest;
-    if (kb < wide_from(epi) || widest <= sub_cols(epi)) return 1;
+int sub_tiles(int epi, Args a, int pairs) {
+    if (a.kb_all < wide_from(epi) || a.p[0].N <= sub_cols(epi)) return 1;
     const int64_t groups = a.G < a.cap ? a.G : a.cap, likely = (a.cap + 255) / 256 + a.G / 2;
     const int64_t row_tiles = likely > groups ? likely : groups;
     const int64_t one = (lay_out(a, epi, 1, row_tiles) + pairs - 1) / pairs, two = (lay_out(a, epi, 2, row_tiles) + pairs - 1) / pairs;
     return 92 * 2 * two <= 100 * one ? 2 : 1;
 }
 
-// `kb`: see sub_tiles.
 template <int EPI, bool B_MN>
-int launch(const Maps& maps, Args a, int kb, cudaStream_t st) {
+int launch(const Maps& maps, Args a, cudaStream_t st) {
     if (a.G < 1 || a.G > kMaxGroups) return -2;
     const WaitSettings wt = wait_settings();
     a.epi_limit = wt.wait_limit ? wt.wait_limit : kWaitLimit;
@@ -1110,7 +1104,7 @@ int launch(const Maps& maps, Args a, int kb, cudaStream_t st) {
     a.wait_limit = a.never_ready ? kWaitLimit : a.epi_limit;
     const int pairs = num_sms() / 2;
     if (pairs < 1) return -3;
-    const int sub = sub_tiles(EPI, a, kb, pairs);
+    const int sub = sub_tiles(EPI, a, pairs);
     // at most this many row tiles: every group's last one may be partial
     const int64_t tiles = lay_out(a, EPI, sub, (a.cap + 255) / 256 + a.G);
     if constexpr (wide_from(EPI) != kNever) {
@@ -1148,7 +1142,7 @@ int launch_train_gate(const bf16* x, const int32_t* off, int64_t rows, int E, in
     m.ah[1] = m.ah[0];
     Args a = token_major(off, rows, E, f, 2 * static_cast<int64_t>(f), gu, ceil_div(d, kBK), ceil_div(d, kBK), status);
     a.h = h;
-    return launch<E_GATE, true>(m, a, a.kb_all, st);
+    return launch<E_GATE, true>(m, a, st);
 }
 
 int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2, float* y,
@@ -1160,7 +1154,7 @@ int launch_train_down(const bf16* h, const int32_t* off, int64_t rows, int E, in
     m.ah[1] = m.ah[0];
     m.b[1] = m.b[0];
     Args a = token_major(off, rows, E, d, d, y, ceil_div(f, kBK), ceil_div(f, kBK), status);
-    return launch<E_F32, true>(m, a, a.kb_all, st);
+    return launch<E_F32, true>(m, a, st);
 }
 
 int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W2,
@@ -1176,7 +1170,7 @@ int launch_train_dgate(const bf16* dy, const int32_t* off, int64_t rows, int E, 
     m.b[1] = m.b[0];
     Args a = token_major(off, rows, E, f, 2 * static_cast<int64_t>(f), dgu, ceil_div(d, kBK), ceil_div(d, kBK), status);
     a.gu = gu;
-    return launch<E_DGATE, false>(m, a, a.kb_all, st);
+    return launch<E_DGATE, false>(m, a, st);
 }
 
 int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, int d, int f, const bf16* W1,
@@ -1189,7 +1183,7 @@ int launch_train_dx(const bf16* dgu, const int32_t* off, int64_t rows, int E, in
         !map_weights(&m.b[0], W1, E, d, f, 128) || !map_weights(&m.b[1], W3, E, d, f, 128))
         return -3;
     Args a = token_major(off, rows, E, d, d, dx, ceil_div(f, kBK), 2 * ceil_div(f, kBK), status);
-    return launch<E_BF16, false>(m, a, a.kb_all, st);
+    return launch<E_BF16, false>(m, a, st);
 }
 
 int launch_train_dw(const WeightGradient* w, int n, const int32_t* off, int64_t chunk, int64_t rows, int G, bool out_bf16,
@@ -1214,20 +1208,15 @@ int launch_train_dw(const WeightGradient* w, int n, const int32_t* off, int64_t 
     a.G = G;
     a.out_bf16 = out_bf16 ? 1 : 0;
     a.status = status;
-    return launch<E_WGRAD, true>(m, a, ceil_div(off ? rows / G : chunk, kBK), st);
+    return launch<E_WGRAD, true>(m, a, st);
 }
 
 int train_subtiles(int product, int64_t rows, int E, int d, int f) {
-    const bool narrow_out = product == E_F32 || product == E_BF16;  // width d, reduction over f
-    const int k = ceil_div(narrow_out ? f : d, kBK) * (product == E_BF16 ? 2 : 1);
-    Args a = token_major(nullptr, rows, E, narrow_out ? d : f, 0, nullptr, k, k, nullptr);
-    if (product == E_WGRAD) {
-        a.products = kProducts;
-        a.p[0].M = a.p[1].M = a.p[2].N = d;
-        a.p[2].M = a.p[0].N = a.p[1].N = f;
-        a.kb_all = ceil_div(rows / E, kBK);
-    }
-    return sub_tiles(product, a, a.kb_all, (num_sms() > 0 ? num_sms() : 148) / 2);
+    if (wide_from(product) == kNever) return 1;
+    const bool gate = product == E_GATE;  // width f, reduction over d; else the other way round
+    const int k = ceil_div(gate ? d : f, kBK) * (product == E_BF16 ? 2 : 1);
+    const Args a = token_major(nullptr, rows, E, gate ? f : d, 0, nullptr, k, k, nullptr);
+    return sub_tiles(product, a, (num_sms() > 0 ? num_sms() : 148) / 2);
 }
 
 }  // namespace moe

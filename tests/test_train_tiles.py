@@ -16,25 +16,29 @@ def tiles(product, T, d, f, E=1, K=1):
 
 def test_large_batches_take_wide_tiles():
     shape = (16384, 4096, 14336, 8, 2)
-    assert [tiles(p, *shape) for p in abi.TRAIN_PRODUCTS] == [2, 2, 1, 2, 2]
-    # short reductions do not
+    assert [tiles(p, *shape) for p in abi.TRAIN_PRODUCTS] == [2, 2, 1, 2, 1]
+    # shorter reductions do not: the down projection's least of all
     assert [tiles(p, 16384, 1024, 512, 64, 2) for p in ("gate", "down", "dx", "dw")] == [1, 1, 1, 1]
+    assert [tiles(p, 16384, 7168, 2048, 16, 2) for p in ("gate", "down", "dx")] == [2, 1, 1]
+    assert [tiles(p, 16384, 4096, 4096, 8, 2) for p in ("gate", "down", "dx")] == [2, 1, 2]
+    assert [tiles("down", 8192, 8192, f) for f in (4096, 8192, 10240, 14336)] == [1, 1, 2, 2]
     # nor outputs of one sub-tile
     assert tiles("down", 65536, 256, 14336) == 1 and tiles("gate", 65536, 8192, 128) == 1
 
 
+@pytest.mark.parametrize("product", ["dgate", "dw"])
 @pytest.mark.parametrize("T,d,f,E,K", [(4096, 8192, 2048, 1, 1), (16384, 16384, 4096, 4, 2), (1 << 20, 65536, 16384, 1, 1)])
-def test_saved_projections_gradient_takes_narrow_tiles(T, d, f, E, K):
-    assert tiles("dgate", T, d, f, E, K) == 1
+def test_narrow_at_any_length(product, T, d, f, E, K):
+    assert tiles(product, T, d, f, E, K) == 1
 
 
 @pytest.mark.parametrize("product,T,d,f,E,K,want", [
     # 16 narrow tiles on 74 pairs, or 8 wide ones that take twice as long
-    ("down", 256, 4096, 14336, 1, 1, 1), ("dx", 256, 4096, 14336, 1, 1, 1), ("down", 128, 2048, 8192, 7, 2, 1), ("dw", 8192, 1024, 1024, 1, 1, 1),
-    # rounds of narrow and wide tiles: (3, 2), (5, 3), (7, 4) and, for all three weight gradients, (11, 6)
-    ("down", 10240, 1024, 4096, 1, 1, 1), ("down", 19456, 1024, 4096, 1, 1, 1), ("dx", 4096, 8192, 2048, 1, 1, 1), ("dw", 8192, 4096, 4096, 1, 1, 1),
-    # (4, 2), (14, 7) and more: wide
-    ("down", 7168, 2048, 4096, 1, 1, 2), ("dx", 4096, 16384, 2048, 1, 1, 2), ("gate", 256, 4096, 14336, 8, 2, 2), ("dx", 8192, 2048, 1408, 60, 4, 2)])
+    ("down", 256, 4096, 14336, 1, 1, 1), ("dx", 256, 4096, 14336, 1, 1, 1), ("gate", 768, 4096, 2048, 1, 1, 1),
+    # rounds of narrow and wide tiles: (3, 2), (5, 3), (7, 4)
+    ("down", 1024, 4096, 14336, 8, 2, 1), ("down", 2048, 4096, 14336, 8, 2, 1), ("dx", 1024, 4096, 8192, 8, 2, 1), ("dx", 4096, 8192, 4096, 1, 1, 1),
+    # (2, 1), (4, 2), (14, 7) and more: wide
+    ("down", 256, 4096, 14336, 8, 2, 2), ("gate", 256, 4096, 14336, 8, 2, 2), ("dx", 4096, 4096, 4096, 1, 1, 2), ("dx", 4096, 16384, 4096, 1, 1, 2)])
 def test_few_tiles_are_not_halved(product, T, d, f, E, K, want):
     assert tiles(product, T, d, f, E, K) == want
 
